@@ -50,6 +50,11 @@ class Layer(ctypes.Structure):
                 ("row_perm", ctypes.c_void_p), ("col_perm", ctypes.c_void_p)]
 
 
+class I8(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("ld", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -57,7 +62,7 @@ def header_functions() -> list[str]:
     """Names of the functions declared in include/mpq.h."""
     txt = open(HEADER).read()
     txt = re.sub(r"/\*.*?\*/", "", txt, flags=re.S)
-    return re.findall(r"\b(mpq_[a-z_]+)\s*\(", txt)
+    return re.findall(r"\b(mpq_[a-z0-9_]+)\s*\(", txt)
 
 
 def lib():
@@ -122,6 +127,19 @@ def load(path: str):
     D.mpq_allocate_bits.restype = ctypes.c_int
     D.mpq_fold_orders.argtypes = [i32, P, P, P]
     D.mpq_fold_orders.restype = ctypes.c_int
+    i64, cint, I8P = ctypes.c_int64, ctypes.c_int, ctypes.POINTER(I8)
+    D.mpq_i8_quantize.argtypes = [P, cint, i64, I8P, P]
+    D.mpq_i8_dequantize.argtypes = [I8P, P, cint, i64, P]
+    D.mpq_i8_linear.argtypes = [I8P, I8P, P, cint, i64, P, sz, P]
+    D.mpq_i8_gated.argtypes = [I8P, I8P, I8P, cint, P, cint, i64, P, sz, P]
+    D.mpq_i8_linear_backward.argtypes = [I8P, P, i32, i64, P, i64, P, sz, P]
+    D.mpq_i8_gated_backward.argtypes = [I8P, I8P, I8P, cint, P, i64, P, P, i64, P, i64, P, sz, P]
+    for f in ("mpq_i8_linear", "mpq_i8_gated", "mpq_i8_linear_backward", "mpq_i8_gated_backward"):
+        getattr(D, f).restype = cint
+        getattr(D, f + "_workspace_size").argtypes = [i32, i32, i32]
+        getattr(D, f + "_workspace_size").restype = sz
+    D.mpq_i8_quantize.restype = cint
+    D.mpq_i8_dequantize.restype = cint
     D.mpq_check.argtypes = [P, P]
     D.mpq_status_string.argtypes = [ctypes.c_int]
     D.mpq_status_string.restype = ctypes.c_char_p
@@ -392,3 +410,239 @@ def check(ws, stream=None):
 
 def table_numpy(P: PackedLayer) -> np.ndarray:
     return P.table.cpu().numpy().view(np.uint32).reshape(-1, 4)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer operators (mpq_i8_*)
+# ---------------------------------------------------------------------------
+ACT_SILU, ACT_GELU_TANH = "silu", "gelu_tanh"
+_ACTS = {ACT_SILU: 0, ACT_GELU_TANH: 1}   # mpq_act
+I8_MAX_COLS = 131071                      # MPQ_I8_MAX_COLS
+
+
+@dataclass
+class I8Matrix:
+    """An int8 matrix in device memory: codes (int8, rows x cols, rows a
+    multiple of 16 bytes apart) and scales (fp32, one a row), plus its C view."""
+    codes: object
+    scales: object
+    c: I8
+
+    @property
+    def rows(self):
+        return self.c.rows
+
+    @property
+    def cols(self):
+        return self.c.cols
+
+
+def _need(ok, where, what):
+    if not ok:
+        raise MpqError(1, "%s: %s" % (where, what))
+
+
+def _tensor_2d(t, where, name, dtypes, device=None, shape=None):
+    """Checks a 2-D CUDA tensor argument with unit column stride; returns its
+    row stride in elements."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dim() == 2, where, "%s must be a 2-D tensor" % name)
+    _need(t.dtype in dtypes, where, "%s has dtype %s" % (name, t.dtype))
+    _need(t.is_cuda, where, "%s must be on a CUDA device" % name)
+    _need(device is None or t.device == device, where, "%s is on another device" % name)
+    _need(shape is None or tuple(t.shape) == tuple(shape), where,
+          "%s is %s, not %s" % (name, tuple(t.shape), shape))
+    rows, cols = t.shape
+    if rows > 1:
+        _need((cols <= 1 or t.stride(1) == 1) and t.stride(0) >= cols, where,
+              "%s must have unit column stride and rows that do not overlap" % name)
+        return t.stride(0)
+    _need(cols <= 1 or t.stride(1) == 1, where, "%s must have unit column stride" % name)
+    return max(cols, 1)
+
+
+def _ydt(t):
+    import torch
+    return Y_BF16 if t.dtype == torch.bfloat16 else Y_F32
+
+
+def i8_matrix(codes, scales) -> I8Matrix:
+    """Wraps existing tensors: codes int8 (rows x cols on cuda, unit column
+    stride, 16-byte aligned rows), scales fp32 (rows).  Shares their memory."""
+    import torch
+    ld = _tensor_2d(codes, "i8_matrix", "codes", (torch.int8,))
+    rows, cols = codes.shape
+    if rows <= 1:
+        ld = (cols + 15) // 16 * 16
+    _need(ld % 16 == 0 and codes.data_ptr() % 16 == 0, "i8_matrix", "rows of codes must be 16-byte aligned")
+    _need(scales.dtype == torch.float32 and scales.device == codes.device and scales.is_contiguous()
+          and tuple(scales.shape) == (rows,), "i8_matrix", "scales must be %d contiguous floats" % rows)
+    return I8Matrix(codes, scales, I8(rows, cols, ld, codes.data_ptr(), scales.data_ptr()))
+
+
+def i8_empty(rows: int, cols: int, device) -> I8Matrix:
+    """An uninitialized int8 matrix (rows padded to 16 bytes)."""
+    import torch
+    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :cols]
+    return i8_matrix(codes, torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def _i8_mat(q, where, name, device=None, cols=None):
+    _need(isinstance(q, I8Matrix), where, "%s must be an I8Matrix" % name)
+    _need(device is None or q.codes.device == device, where, "%s is on another device" % name)
+    if cols is not None and q.cols != cols:
+        raise MpqError(2, "%s: %s has %d columns, not %d" % (where, name, q.cols, cols))
+    return q
+
+
+def _on(device, stream):
+    """The device guard and stream handle of a call on tensors of `device`."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    _need(s.device == device, "stream", "the stream is on another device than the tensors")
+    return torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+
+
+def _i8_ws(ws, size, device, where):
+    import torch
+    if ws is None:
+        return torch.zeros(size, dtype=torch.uint8, device=device)
+    _need(ws.is_cuda and ws.device == device and ws.is_contiguous(), where, "ws is not contiguous on the device")
+    return ws
+
+
+def _i8_call(name, device, stream, ws, size, *args):
+    guard, s = _on(device, stream)
+    with guard:
+        w = _i8_ws(ws, size, device, name)
+        if stream is not None and ws is None:
+            w.record_stream(stream)      # allocated here, used on the caller's stream
+            import torch
+            stream.wait_stream(torch.cuda.current_stream(device))   # its zero fill
+        _raise(getattr(lib(), name)(*args, w.data_ptr(), w.numel() * w.element_size(), s), name)
+
+
+def _out(out, shape, device, where, name, dtypes, stream):
+    import torch
+    if out is None:
+        out = torch.empty(shape, dtype=dtypes[0], device=device)
+        if stream is not None:
+            out.record_stream(stream)
+            stream.wait_stream(torch.cuda.current_stream(device))   # the memory's earlier uses
+    return out, _tensor_2d(out, where, name, dtypes, device, shape)
+
+
+def i8_quantize(x, out: I8Matrix = None, stream=None) -> I8Matrix:
+    """mpq_i8_quantize: rows of x (bf16 or fp32, cuda) to int8 codes with one
+    scale a row."""
+    import torch
+    ldx = _tensor_2d(x, "i8_quantize", "x", (torch.bfloat16, torch.float32))
+    if out is None:
+        out = i8_empty(x.shape[0], x.shape[1], x.device)
+        if stream is not None:
+            for t in (out.codes, out.scales):
+                t.record_stream(stream)
+            stream.wait_stream(torch.cuda.current_stream(x.device))
+    _i8_mat(out, "i8_quantize", "out", x.device, x.shape[1])
+    _need(out.rows == x.shape[0], "i8_quantize", "out has %d rows, not %d" % (out.rows, x.shape[0]))
+    guard, s = _on(x.device, stream)
+    with guard:
+        _raise(lib().mpq_i8_quantize(x.data_ptr(), _ydt(x), ldx, ctypes.byref(out.c), s), "mpq_i8_quantize")
+    return out
+
+
+def i8_dequantize(q: I8Matrix, out=None, stream=None, ydtype: int = Y_F32):
+    """mpq_i8_dequantize: codes * scales in fp32, or bf16 (out's type, or ydtype)."""
+    import torch
+    _i8_mat(q, "i8_dequantize", "q")
+    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
+    dev = q.codes.device
+    out, ld = _out(out, (q.rows, q.cols), dev, "i8_dequantize", "out", dts, stream)
+    guard, s = _on(dev, stream)
+    with guard:
+        _raise(lib().mpq_i8_dequantize(ctypes.byref(q.c), out.data_ptr(), _ydt(out), ld, s), "mpq_i8_dequantize")
+    return out
+
+
+def i8_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return lib().mpq_i8_linear_workspace_size(M, N, K)
+
+
+def i8_gated_workspace_size(M: int, F: int, K: int) -> int:
+    return lib().mpq_i8_gated_workspace_size(M, F, K)
+
+
+def i8_linear_backward_workspace_size(M: int, N: int, K: int) -> int:
+    return lib().mpq_i8_linear_backward_workspace_size(M, N, K)
+
+
+def i8_gated_backward_workspace_size(M: int, F: int, K: int) -> int:
+    return lib().mpq_i8_gated_backward_workspace_size(M, F, K)
+
+
+def i8_linear(x: I8Matrix, w: I8Matrix, out=None, ws=None, stream=None, ydtype: int = Y_F32):
+    """mpq_i8_linear: y (M x N, fp32 or bf16: out's type, or ydtype) = x_hat * w_hat^T."""
+    import torch
+    dev = _i8_mat(x, "i8_linear", "x").codes.device
+    _i8_mat(w, "i8_linear", "w", dev, x.cols)
+    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
+    out, ld = _out(out, (x.rows, w.rows), dev, "i8_linear", "out", dts, stream)
+    _i8_call("mpq_i8_linear", dev, stream, ws, i8_linear_workspace_size(x.rows, w.rows, x.cols),
+             ctypes.byref(x.c), ctypes.byref(w.c), out.data_ptr(), _ydt(out), ld)
+    return out
+
+
+def _act(act, where):
+    _need(act in _ACTS, where, "act must be one of %s" % sorted(_ACTS))
+    return _ACTS[act]
+
+
+def i8_gated(x: I8Matrix, w_gate: I8Matrix, w_up: I8Matrix, act: str = ACT_SILU, out=None, ws=None,
+             stream=None, ydtype: int = Y_BF16):
+    """mpq_i8_gated: h (M x F, bf16 or fp32: out's type, or ydtype) =
+    act(x_hat * w_gate_hat^T) * (x_hat * w_up_hat^T)."""
+    import torch
+    dev = _i8_mat(x, "i8_gated", "x").codes.device
+    for n, w in (("w_gate", w_gate), ("w_up", w_up)):
+        _i8_mat(w, "i8_gated", n, dev, x.cols)
+    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
+    out, ld = _out(out, (x.rows, w_gate.rows), dev, "i8_gated", "out", dts, stream)
+    _i8_call("mpq_i8_gated", dev, stream, ws, i8_gated_workspace_size(x.rows, w_gate.rows, x.cols),
+             ctypes.byref(x.c), ctypes.byref(w_gate.c), ctypes.byref(w_up.c), _act(act, "i8_gated"),
+             out.data_ptr(), _ydt(out), ld)
+    return out
+
+
+def i8_linear_backward(w: I8Matrix, dy, out=None, ws=None, stream=None):
+    """mpq_i8_linear_backward: dx (bf16, M x K) = dy (bf16, M x N) * w_hat."""
+    import torch
+    bf = (torch.bfloat16,)
+    dev = _i8_mat(w, "i8_linear_backward", "w").codes.device
+    lddy = _tensor_2d(dy, "i8_linear_backward", "dy", bf, dev)
+    if dy.shape[1] != w.rows:
+        raise MpqError(2, "i8_linear_backward: dy has %d columns, not %d" % (dy.shape[1], w.rows))
+    out, ld = _out(out, (dy.shape[0], w.cols), dev, "i8_linear_backward", "out", bf, stream)
+    _i8_call("mpq_i8_linear_backward", dev, stream, ws,
+             i8_linear_backward_workspace_size(dy.shape[0], w.rows, w.cols),
+             ctypes.byref(w.c), dy.data_ptr(), dy.shape[0], lddy, out.data_ptr(), ld)
+    return out
+
+
+def i8_gated_backward(x: I8Matrix, w_gate: I8Matrix, w_up: I8Matrix, dh, act: str = ACT_SILU, dx=None,
+                      d_gate=None, d_up=None, ws=None, stream=None):
+    """mpq_i8_gated_backward: (dx, d_gate, d_up), all bf16, from dh (bf16, M x F)."""
+    import torch
+    where, bf = "i8_gated_backward", (torch.bfloat16,)
+    dev = _i8_mat(x, where, "x").codes.device
+    for n, w in (("w_gate", w_gate), ("w_up", w_up)):
+        _i8_mat(w, where, n, dev, x.cols)
+    M, F = x.rows, w_gate.rows
+    lddh = _tensor_2d(dh, where, "dh", bf, dev, (M, F))
+    dx, lddx = _out(dx, (M, x.cols), dev, where, "dx", bf, stream)
+    d_gate, ldg = _out(d_gate, (M, F), dev, where, "d_gate", bf, stream)
+    d_up, ldu = _out(d_up, (M, F), dev, where, "d_up", bf, stream)
+    _need(ldg == ldu, where, "d_gate and d_up must have the same row stride")
+    _i8_call("mpq_i8_gated_backward", dev, stream, ws, i8_gated_backward_workspace_size(M, F, x.cols),
+             ctypes.byref(x.c), ctypes.byref(w_gate.c), ctypes.byref(w_up.c), _act(act, where), dh.data_ptr(),
+             lddh, d_gate.data_ptr(), d_up.data_ptr(), ldg, dx.data_ptr(), lddx)
+    return dx, d_gate, d_up

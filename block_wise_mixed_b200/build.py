@@ -13,9 +13,9 @@ LIB = os.path.join(PKG, "libmpq.so")
 # the producers issue no copies, so calls end with MPQ_ERR_TIMEOUT; used only
 # by the timeout test (tests/test_gpu_timeout.py), never by the package.
 WAIT_TEST_LIB = os.path.join(PKG, "libmpq_waittest.so")
-SOURCES = [os.path.join(PKG, "csrc", "mpq_api.cu")]
+SOURCES = [os.path.join(PKG, "csrc", "mpq_api.cu"), os.path.join(PKG, "csrc", "mpq_i8.cu")]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
-              "-lineinfo", "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v"]
+              "-lineinfo", "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v", "-t", "0"]
 
 
 def _deps():

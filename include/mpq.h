@@ -363,6 +363,103 @@ mpq_status mpq_allocate_bits(int64_t n_blocks, const float* loss_dev, uint32_t a
 mpq_status mpq_fold_orders(int32_t n, const int32_t* row_perm_a, const int32_t* col_perm_b,
                            int32_t* out);
 
+/* ------------------------------------------------------------------------
+ * 8-bit integer operators (native integer computation: TileQuant abstract).
+ * A layer that stays at 8 bits throughout needs no block table: its codes
+ * are one int8 matrix with one scale for each output channel, and its
+ * activations are quantized as they come, with one scale for each token.
+ *
+ *   x_hat[r][c] = scales[r] * codes[r][c]
+ *
+ * The operators read and write such matrices in the layout below, next to
+ * the packed layers: mpq_i8_quantize takes the fp32 output of mpq_linear or
+ * a bf16 hidden state, and mpq_i8_gated's bf16 output is an mpq_linear input.
+ * ------------------------------------------------------------------------ */
+
+/* An int8 matrix in device memory: tokens of the activations or output
+ * channels of the weights as rows.  codes is 16-byte aligned, rows are ld
+ * bytes apart (ld a multiple of 16, >= cols; the bytes behind a row's last
+ * column are neither read nor written), scales holds rows floats (4-byte
+ * aligned).  1 <= cols <= MPQ_I8_MAX_COLS: the products' sums of cols terms
+ * of up to 128 * 128 are exact in 32 bits. */
+#define MPQ_I8_MAX_COLS 131071
+typedef struct {
+    int32_t rows, cols;
+    int64_t ld;
+    const int8_t* codes;
+    const float* scales;
+} mpq_i8;
+
+/* The gate of mpq_i8_gated: silu(a) = a / (1 + exp(-a)), or gelu_tanh(a) =
+ * a (1 + tanh(u)) / 2 with u = sqrt(2 / pi) (a + 0.044715 a^3). */
+typedef enum { MPQ_ACT_SILU = 0, MPQ_ACT_GELU_TANH = 1 } mpq_act;
+
+/* Quantizes the rows of x (fp32 or bf16 bit patterns by `dt`; element (r, c)
+ * at r * ldx + c, ldx >= cols, any alignment of the element type) into
+ * out->codes and out->scales:
+ *   amax = max_c |x[r][c]|,  s = max(fl32(amax / 127), 2^-126), s = 1 if
+ *   amax == 0;  code = the integer nearest to the exact quotient x / s, ties
+ *   to even (within -127..127).
+ * A row with a NaN or an infinity gets the scale NaN and codes 0, so that
+ * what is computed from it is NaN and other rows are not touched.
+ * Errors: ARG, SHAPE (rows < 0, cols out of range); rows == 0 is a no-op. */
+mpq_status mpq_i8_quantize(const void* x_dev, mpq_ydtype dt, int64_t ldx, const mpq_i8* out,
+                           void* stream);
+
+/* Reads an int8 matrix back: x[r][c] = scales[r] * codes[r][c], the fp32
+ * product, rounded to nearest-even for MPQ_Y_BF16.  Errors as above. */
+mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_t ldx, void* stream);
+
+/* y = x_hat * w_hat^T with scales for each token and channel:
+ *   y[m][n] = (sum_k x.codes[m][k] * w.codes[n][k]) * w.scales[n] * x.scales[m]
+ * (the sum is exact in int32, then fp32 in the order written; rounded to
+ * nearest-even for MPQ_Y_BF16).  x: M x K, w: N x K; y element (m, n) at
+ * m * ldy + n (ldy >= N), aligned to its type.
+ *   ws  device workspace of mpq_i8_linear_workspace_size(M, N, K) bytes,
+ *       256-byte aligned, zero-filled before its first use: the same rules
+ *       as mpq_linear's (left clean by every call without a device error;
+ *       not shared by calls that may overlap).
+ * Results do not depend on how the work is split.  Host errors: ARG, SHAPE
+ * (columns differ, sizes out of range), WORKSPACE; device (mpq_check):
+ * TIMEOUT.  M == 0 is a no-op. */
+size_t mpq_i8_linear_workspace_size(int32_t M, int32_t N, int32_t K);
+mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydtype ydt, int64_t ldy,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Gated feed-forward block up to its down projection, in one kernel:
+ *   a = x_hat * w_gate_hat^T,  b = x_hat * w_up_hat^T   (as mpq_i8_linear)
+ *   h = act(a) * b                                      (fp32, then ydt)
+ * x: M x K, w_gate and w_up: F x K; h element (m, f) at m * ldh + f.
+ * Workspace rules and errors as for mpq_i8_linear. */
+size_t mpq_i8_gated_workspace_size(int32_t M, int32_t F, int32_t K);
+mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_up, mpq_act act,
+                        void* h_dev, mpq_ydtype ydt, int64_t ldh, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Backward passes with respect to the activations; codes and scales are
+ * constants (the quantizer's gradient is taken as one).  Gradients are bf16
+ * in and out and accumulated in fp32; a gradient that enters a product is
+ * rounded to bf16 once, after its channel's scale is applied, and the codes
+ * are exact in bf16.
+ *
+ * mpq_i8_linear_backward:  dx[m][k] = sum_n (dy[m][n] w.scales[n]) w.codes[n][k]
+ *   dy: M x N (element (m, n) at m * lddy + n), dx: M x K (lddx).
+ * mpq_i8_gated_backward:   with a and b computed again from x,
+ *   d_gate = dh * b * act'(a),  d_up = dh * act(a)       (M x F, ldd each)
+ *   dx = sum_f (d_gate s_gate) gate.codes + (d_up s_up) up.codes   (M x K)
+ *   d_gate and d_up (for adapters next to the frozen layers) may both be
+ *   NULL; dx's products round the fp32 values, not the bf16 outputs.
+ * Workspace rules and errors as for mpq_i8_linear.  Outputs must not overlap
+ * inputs. */
+size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K);
+mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M, int64_t lddy,
+                                  void* dx_dev, int64_t lddx, void* ws, size_t ws_bytes, void* stream);
+size_t mpq_i8_gated_backward_workspace_size(int32_t M, int32_t F, int32_t K);
+mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_up, mpq_act act,
+                                 const void* dh_dev, int64_t lddh, void* d_gate_dev, void* d_up_dev,
+                                 int64_t ldd, void* dx_dev, int64_t lddx, void* ws, size_t ws_bytes,
+                                 void* stream);
+
 /* Synchronizes `stream` and returns the device error word of `ws`: the first
  * device error of the mpq_linear calls on that workspace since it was
  * zero-filled or since the previous mpq_check, or of the last mpq_pack

@@ -1,0 +1,175 @@
+"""Host-side checks of the 8-bit integer operators that need no GPU: argument
+validation through the C ABI (no call here reaches a launch), workspace sizes
+and the binding's tensor checks."""
+import ctypes
+
+import pytest
+
+from block_wise_mixed_b200 import _lib as B
+from block_wise_mixed_b200 import build
+
+P = ctypes.c_void_p
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return B.lib()
+
+
+def mat(rows=4, cols=64, ld=None, codes=16, scales=16):
+    return B.I8(rows, cols, (cols + 15) // 16 * 16 if ld is None else ld, codes, scales)
+
+
+def ref(m):
+    return None if m is None else ctypes.byref(m)
+
+
+def status(st):
+    return B.STATUS[st]
+
+
+def test_header_declares_and_library_exports(lib):
+    names = set(B.header_functions())
+    want = {"mpq_i8_quantize", "mpq_i8_dequantize", "mpq_i8_linear", "mpq_i8_gated", "mpq_i8_linear_backward",
+            "mpq_i8_gated_backward"}
+    want |= {n + "_workspace_size" for n in want if "quantize" not in n}
+    assert want <= names
+    for n in want:
+        assert hasattr(lib, n)
+
+
+def test_struct_size():
+    assert ctypes.sizeof(B.I8) == 32
+
+
+# what every call refuses in an int8 matrix
+BAD = [
+    (dict(rows=-1), "MPQ_ERR_SHAPE"), (dict(cols=0), "MPQ_ERR_SHAPE"), (dict(cols=131072), "MPQ_ERR_SHAPE"),
+    (dict(ld=48), "MPQ_ERR_ARG"), (dict(cols=60, ld=60), "MPQ_ERR_ARG"), (dict(codes=None), "MPQ_ERR_ARG"),
+    (dict(codes=24), "MPQ_ERR_ARG"), (dict(scales=None), "MPQ_ERR_ARG"), (dict(scales=18), "MPQ_ERR_ARG"),
+]
+
+
+@pytest.mark.parametrize("kw,err", BAD)
+def test_bad_matrices(lib, kw, err):
+    bad, good = mat(**kw), mat()
+    q = lib.mpq_i8_quantize
+    assert status(q(P(16), 0, 1 << 20, ref(bad), None)) == err
+    assert status(lib.mpq_i8_dequantize(ref(bad), P(16), 0, 1 << 20, None)) == err
+    for x, w in ((bad, good), (good, bad)):
+        assert status(lib.mpq_i8_linear(ref(x), ref(w), P(16), 0, 1 << 20, P(256), BIG, None)) == err
+    for x, g, u in ((bad, good, good), (good, bad, good), (good, good, bad)):
+        assert status(lib.mpq_i8_gated(ref(x), ref(g), ref(u), 0, P(16), 1, 1 << 20, P(256), BIG, None)) == err
+        assert status(lib.mpq_i8_gated_backward(ref(x), ref(g), ref(u), 0, P(16), 1 << 20, P(16), P(16), 1 << 20,
+                                                P(16), 1 << 20, P(256), BIG, None)) == err
+    assert status(lib.mpq_i8_linear_backward(ref(bad), P(16), 4, 1 << 20, P(16), 1 << 20, P(256), BIG, None)) == err
+
+
+def test_rows(lib):
+    m = mat()
+    q, d = lib.mpq_i8_quantize, lib.mpq_i8_dequantize
+    assert status(q(P(16), 0, 64, None, None)) == "MPQ_ERR_ARG"
+    assert status(q(None, 0, 64, ref(m), None)) == "MPQ_ERR_ARG"
+    assert status(q(P(16), 2, 64, ref(m), None)) == "MPQ_ERR_ARG"     # no such type
+    assert status(q(P(16), 0, 63, ref(m), None)) == "MPQ_ERR_ARG"     # rows overlap
+    assert status(q(P(18), 0, 64, ref(m), None)) == "MPQ_ERR_ARG"     # fp32 at an odd half word
+    assert status(q(P(17), 1, 64, ref(m), None)) == "MPQ_ERR_ARG"
+    assert status(d(ref(m), None, 0, 64, None)) == "MPQ_ERR_ARG"
+    assert status(d(ref(m), P(16), 3, 64, None)) == "MPQ_ERR_ARG"
+    assert status(d(ref(m), P(16), 0, 63, None)) == "MPQ_ERR_ARG"
+    empty = mat(rows=0, codes=None, scales=None)
+    assert q(None, 0, 64, ref(empty), None) == 0
+    assert d(ref(empty), None, 0, 64, None) == 0
+
+
+def test_linear(lib):
+    x, w = mat(rows=5), mat(rows=96)
+    f = lib.mpq_i8_linear
+    need = lib.mpq_i8_linear_workspace_size(5, 96, 64)
+
+    def call(x=x, w=w, y=16, dt=0, ldy=96, ws=256, size=need):
+        return status(f(ref(x), ref(w), P(y) if y else None, dt, ldy, P(ws) if ws else None, size, None))
+    assert need >= 256
+    assert call(x=None) == "MPQ_ERR_ARG" and call(w=None) == "MPQ_ERR_ARG"
+    assert call(y=None) == "MPQ_ERR_ARG" and call(y=18) == "MPQ_ERR_ARG" and call(y=17, dt=1) == "MPQ_ERR_ARG"
+    assert call(dt=2) == "MPQ_ERR_ARG" and call(dt=-1) == "MPQ_ERR_ARG"
+    assert call(ldy=95) == "MPQ_ERR_ARG"
+    assert call(ws=None) == "MPQ_ERR_WORKSPACE" and call(ws=128) == "MPQ_ERR_WORKSPACE"
+    assert call(size=need - 1) == "MPQ_ERR_WORKSPACE"
+    assert call(w=mat(rows=96, cols=65)) == "MPQ_ERR_SHAPE"
+    assert call(w=mat(rows=0, codes=None, scales=None)) == "MPQ_ERR_SHAPE"
+    assert call(x=mat(rows=0, codes=None, scales=None), y=None, ws=None) == "MPQ_OK"
+
+
+def test_gated(lib):
+    x, g, u = mat(rows=5), mat(rows=96), mat(rows=96)
+    need = lib.mpq_i8_gated_workspace_size(5, 96, 64)
+
+    def call(x=x, g=g, u=u, act=0, y=16, dt=1, ldy=96, ws=256, size=need):
+        return status(lib.mpq_i8_gated(ref(x), ref(g), ref(u), act, P(y) if y else None, dt, ldy,
+                                       P(ws) if ws else None, size, None))
+    assert call(g=None) == "MPQ_ERR_ARG" and call(u=None) == "MPQ_ERR_ARG"
+    assert call(act=2) == "MPQ_ERR_ARG" and call(act=-1) == "MPQ_ERR_ARG" and call(dt=2) == "MPQ_ERR_ARG"
+    assert call(u=mat(rows=95)) == "MPQ_ERR_SHAPE" and call(u=mat(rows=96, cols=63)) == "MPQ_ERR_SHAPE"
+    assert call(ldy=95) == "MPQ_ERR_ARG" and call(y=None) == "MPQ_ERR_ARG"
+    assert call(ws=None) == "MPQ_ERR_WORKSPACE" and call(size=need - 1) == "MPQ_ERR_WORKSPACE"
+    assert call(x=mat(rows=0, codes=None, scales=None), y=None, ws=None) == "MPQ_OK"
+
+
+def test_backward(lib):
+    w = mat(rows=96)
+    need = lib.mpq_i8_linear_backward_workspace_size(5, 96, 64)
+
+    def lin(w=w, dy=16, M=5, lddy=96, dx=16, lddx=64, ws=256, size=need):
+        return status(lib.mpq_i8_linear_backward(ref(w), P(dy) if dy else None, M, lddy, P(dx) if dx else None, lddx,
+                                                 P(ws) if ws else None, size, None))
+    assert lin(w=None) == "MPQ_ERR_ARG" and lin(dy=None) == "MPQ_ERR_ARG" and lin(dx=None) == "MPQ_ERR_ARG"
+    assert lin(dy=17) == "MPQ_ERR_ARG" and lin(dx=17) == "MPQ_ERR_ARG"
+    assert lin(lddy=95) == "MPQ_ERR_ARG" and lin(lddx=63) == "MPQ_ERR_ARG"
+    assert lin(M=-1) == "MPQ_ERR_SHAPE" and lin(M=0, dy=None, dx=None, ws=None) == "MPQ_OK"
+    assert lin(w=mat(rows=0, codes=None, scales=None)) == "MPQ_ERR_SHAPE"
+    assert lin(ws=None) == "MPQ_ERR_WORKSPACE" and lin(size=need - 1) == "MPQ_ERR_WORKSPACE"
+
+    x, g, u = mat(rows=5), mat(rows=96), mat(rows=96)
+    need = lib.mpq_i8_gated_backward_workspace_size(5, 96, 64)
+
+    def gat(x=x, g=g, u=u, act=0, dh=16, lddh=96, dg=16, du=16, ldd=96, dx=16, lddx=64, ws=256, size=need):
+        pp = [P(v) if v else None for v in (dh, dg, du, dx, ws)]
+        return status(lib.mpq_i8_gated_backward(ref(x), ref(g), ref(u), act, pp[0], lddh, pp[1], pp[2], ldd, pp[3],
+                                                lddx, pp[4], size, None))
+    assert gat(act=2) == "MPQ_ERR_ARG" and gat(dh=None) == "MPQ_ERR_ARG" and gat(dx=None) == "MPQ_ERR_ARG"
+    assert gat(dg=None) == "MPQ_ERR_ARG" and gat(du=None) == "MPQ_ERR_ARG"      # both or neither
+    assert gat(lddh=95) == "MPQ_ERR_ARG" and gat(ldd=95) == "MPQ_ERR_ARG" and gat(lddx=63) == "MPQ_ERR_ARG"
+    assert gat(dg=17) == "MPQ_ERR_ARG" and gat(du=17) == "MPQ_ERR_ARG"
+    assert gat(u=mat(rows=95)) == "MPQ_ERR_SHAPE" and gat(x=mat(rows=5, cols=65)) == "MPQ_ERR_SHAPE"
+    assert gat(ws=None) == "MPQ_ERR_WORKSPACE" and gat(size=need - 1) == "MPQ_ERR_WORKSPACE"
+    assert gat(x=mat(rows=0, codes=None, scales=None), dh=None, dx=None, ws=None) == "MPQ_OK"
+
+
+@pytest.mark.parametrize("name", ["linear", "gated", "linear_backward", "gated_backward"])
+def test_workspace_sizes(lib, name):
+    f = getattr(lib, "mpq_i8_%s_workspace_size" % name)
+    for bad in ((-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 131072)):
+        assert f(*bad) == 0
+    for M in (0, 1, 17, 300, 5000):
+        for N, K in ((1, 1), (1371, 2003), (28672, 8192)):
+            assert f(M, N, K) >= 256 and f(M, N, K) % 256 == 0
+
+
+def test_binding_refuses(lib):
+    """Tensor checks of the binding; they raise before the library is called."""
+    import torch
+    x = torch.zeros(4, 64)
+    with pytest.raises(B.MpqError) as ei:
+        B.i8_quantize(x)                       # not on a CUDA device
+    assert ei.value.name == "MPQ_ERR_ARG"
+    with pytest.raises(B.MpqError):
+        B.i8_quantize(x.half())                # neither bf16 nor fp32
+    with pytest.raises(B.MpqError):
+        B.i8_quantize(x[0])                    # one dimension
+    with pytest.raises(B.MpqError):
+        B.i8_matrix(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4))
+    with pytest.raises(B.MpqError):
+        B.i8_linear(x, x)                      # no int8 matrices
