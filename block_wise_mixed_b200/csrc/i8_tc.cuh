@@ -1,0 +1,173 @@
+// i8_tc.cuh -- tcgen05 / TMA / cluster helpers of the int8 kernels.
+#pragma once
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace mpq {
+
+// As in k_decode.cuh: bounded waits; the wait-test build gives up after 2 ms
+// and its producers arm their barriers without issuing a copy.
+#ifdef MPQ_WAIT_TEST
+constexpr bool kI8WaitTest = true;
+constexpr uint64_t I8_WAIT_NS = 2000000ull;
+#else
+constexpr bool kI8WaitTest = false;
+constexpr uint64_t I8_WAIT_NS = 2000000000ull;
+#endif
+
+// Shared-memory operand, K-major, 128-byte swizzle: 8-row groups 1024 bytes
+// apart, descriptor version 1, layout type 2.
+__device__ __forceinline__ uint64_t i8_smem_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// Instruction descriptors, both operands K-major: s8 x s8 -> s32, and
+// bf16 x bf16 -> fp32.
+__host__ __device__ constexpr uint32_t i8_idesc(int M, int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t bf16_idesc(int M, int N) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// KIND 0: i8, 1: f16 (bf16 operands).  PAIR: the two SMs of a cluster.
+template <bool PAIR, int KIND>
+__device__ __forceinline__ void i8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#define MPQ_I8_MMA(GROUP, K)                                                      \
+    asm volatile(                                                                 \
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                         \
+        "tcgen05.mma.cta_group::" GROUP ".kind::" K " [%0], %1, %2, %3, p;\n\t}"  \
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory")
+    if (PAIR) {
+        if (KIND == 0) MPQ_I8_MMA("2", "i8");
+        else MPQ_I8_MMA("2", "f16");
+    } else {
+        if (KIND == 0) MPQ_I8_MMA("1", "i8");
+        else MPQ_I8_MMA("1", "f16");
+    }
+#undef MPQ_I8_MMA
+}
+
+// Arrive on `bar` (PAIR: on the barrier at the same address in both CTAs)
+// when the MMAs issued so far by this thread are done.
+template <bool PAIR>
+__device__ __forceinline__ void i8_commit(uint64_t* bar) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void i8_tmem_alloc(uint32_t* dst, uint32_t cols) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void i8_tmem_free(uint32_t addr, uint32_t cols) {
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void i8_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void i8_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 / 32 consecutive 32-bit columns of the warp's 32 lanes, completed by
+// i8_tmem_wait().
+__device__ __forceinline__ void i8_tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void i8_tmem_ld32(uint32_t taddr, uint32_t* r) {
+    i8_tmem_ld16(taddr, r);
+    i8_tmem_ld16(taddr + 16u, r + 16);
+}
+__device__ __forceinline__ void i8_tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Cluster of two.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The waits on arrivals from the peer CTA.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+                : "memory");
+            if (ok) return true;
+        }
+        if (global_timer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+// Tensor-map copies global -> own shared memory.  PAIR: completes on a
+// barrier of either CTA of the cluster (bar: shared::cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void i8_tma_load(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+}
+__device__ __forceinline__ void i8_tma_prefetch(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// After an abort: gives copies and arrivals in flight, which no barrier of
+// this CTA tracks any more, time to land before the memory is given up.
+__device__ __forceinline__ void i8_settle() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {}
+}
+
+}  // namespace mpq

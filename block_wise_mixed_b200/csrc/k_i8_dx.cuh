@@ -1,0 +1,371 @@
+// k_i8_dx.cuh -- gradients through int8 weights:
+//
+//   dx[m][k] = sum_n g[m][n] w[n][k]     (g = gradient times channel scale)
+//
+// for one weight matrix, or for gate and up as one contraction over both
+// matrices' channels.  g is bf16 and the codes are exact in bf16, so the
+// products run on tcgen05.mma kind::f16 with fp32 sums, 256 k columns x NT
+// tokens over the two SMs of a cluster.
+//
+// The codes lie with k along the rows and the contraction across them; the
+// operand wants the contraction along its rows, in bf16.  Eight warps turn
+// each 64 x 128 code tile (8 KB, by TMA) into the swizzled 128 x 64 operand:
+// a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
+// one byte permute, and makes them bf16 with two masks and one subtraction:
+//   code = bf16(0x4300 | (b & 0x7F)) - bf16(0x4300 | (b & 0x80))
+// (128 + low bits, less 128 or 256: exact).  Lanes are laid out so that both
+// the 4-byte reads and the 16-byte writes use all banks.  A weight byte
+// crosses HBM once for NT tokens and is never stored wider.
+//
+// Work is cut as in k_i8_stream (equal runs of 64-row units, one a pair); the
+// fp32 partial sums of a cut tile are added in the order of the runs by the
+// last contributor, whoever that is, so results are reproducible.
+//
+// Roles: warp 0 copies, warp 1 of the first CTA issues, warps 2-5 finish
+// (lane = k column), warps 6-13 convert.  Every wait is bounded.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "k_i8_stream.cuh"
+
+namespace mpq {
+
+constexpr int I8X_CONV = 8;
+constexpr int I8X_WARPS = 6 + I8X_CONV;
+constexpr int I8X_NC = 64;                  // channels in a stage
+constexpr int I8X_RAW = I8X_NC * 128;       // codes of a stage
+constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
+
+template <int NT>
+struct I8DxCfg {
+    static constexpr int B = NT / 2 * I8X_NC * 2;              // this CTA's tokens
+    static constexpr int R = 6;                                // code stages
+    static constexpr int S = NT == 256 ? 5 : 6;                // operand stages
+    static constexpr uint32_t COLS = 2 * NT;                   // double-buffered accumulator
+};
+
+template <int NT>
+struct I8DxSmem {
+    using Cfg = I8DxCfg<NT>;
+    uint8_t a[Cfg::S][I8X_A];               // 1024-aligned
+    uint8_t b[Cfg::S][(Cfg::B + 1023) / 1024 * 1024];
+    uint8_t raw[Cfg::R][I8X_RAW];
+    uint64_t raw_full[Cfg::R], raw_empty[Cfg::R];
+    uint64_t a_full[Cfg::S], b_full[Cfg::S], empty[Cfg::S];
+    uint64_t d_full[2], d_empty[2], drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+};
+
+struct I8DxParams {
+    uint16_t* dx;
+    int64_t lddx;
+    int M, N, K, nw;
+    uint32_t* err;
+    uint32_t* counters;
+    float* slots;
+};
+
+// Bytes j of two rows' words as a pair of bf16 values.
+__device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j) {
+    const uint32_t t = __byte_perm(wa, wb, (uint32_t)(j | (j << 4) | ((4 + j) << 8) | ((4 + j) << 12)));
+    const uint32_t lo = lop_and_or(t, 0x007F007Fu, 0x43004300u), hi = lop_and_or(t, 0x00800080u, 0x43004300u);
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&hi));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8X_WARPS * 32, 1)
+k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
+        const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p) {
+    using Cfg = I8DxCfg<NT>;
+    constexpr int S = Cfg::S, R = Cfg::R;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    I8DxSmem<NT>& sm = *reinterpret_cast<I8DxSmem<NT>*>(base);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+
+    const int NB = (p.N + I8X_NC - 1) / I8X_NC, C = NB * p.nw;
+    const int64_t TK = (p.K + 255) / 256, TM = (p.M + NT - 1) / NT;
+    const int64_t units = TK * TM * C, G = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int64_t u0 = i8_run_start(pair, units, G), u1 = i8_run_start(pair + 1, units, G);
+
+    if (tid == 0) {
+        for (int s = 0; s < R; ++s) {
+            mbar_init(&sm.raw_full[s], 1);
+            mbar_init(&sm.raw_empty[s], I8X_CONV);
+        }
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sm.a_full[s], 2 * I8X_CONV);
+            mbar_init(&sm.b_full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.d_full[b], 1);
+            mbar_init(&sm.d_empty[b], 8);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+        i8_tma_prefetch(&wmap0);
+        i8_tma_prefetch(&gmap0);
+    }
+    if (warp == 1) i8_tmem_alloc<true>(&sm.tmem, Cfg::COLS);
+    i8_fence_before();
+    __syncthreads();
+    cluster_sync();
+    i8_fence_after();
+    const uint32_t tmem = sm.tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    auto timed_out = [&]() {
+        set_error(p.err, MPQ_ERR_TIMEOUT);
+        sm.abort_flag = 1;
+    };
+    int armed = 0;   // units whose copies were issued
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int64_t u = u0; u < u1; ++u) {
+                const int64_t tile = u / C;
+                const int c = (int)(u % C), j = c / NB, n = (c % NB) * I8X_NC;
+                const int k0 = (int)(tile / TM) * 256 + (int)rank * 128;
+                const int m0 = (int)((tile % TM) * NT + rank * (NT / 2));
+                const int r = armed % R, s = armed % S;
+                bool ok = !sm.abort_flag &&
+                          mbar_wait_bounded(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u, I8_WAIT_NS);
+                if (!ok) {
+                    if (!sm.abort_flag) timed_out();
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.raw_full[r], I8X_RAW);
+                if (kI8WaitTest) break;   // armed, no copy
+                i8_tma_load<false>(sm.raw[r], j ? &wmap1 : &wmap0, k0, n, smem_u32(&sm.raw_full[r]));
+                ok = mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS);
+                if (!ok) {
+                    timed_out();
+                    break;
+                }
+                if (rank == 0) mbar_arrive_expect_tx(&sm.b_full[s], 2 * Cfg::B);
+                i8_tma_load<true>(sm.b[s], j ? &gmap1 : &gmap0, n, m0, cluster_addr(&sm.b_full[s], 0));
+                ++armed;
+            }
+            if (!sm.abort_flag && !kI8WaitTest)
+                for (int i = max(0, armed - S); i < armed; ++i)
+                    if (!mbar_wait_bounded(&sm.empty[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS)) {
+                        timed_out();
+                        break;
+                    }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = bf16_idesc(256, NT);
+            int it = 0, seg = 0;
+            bool ok = true;
+            for (int64_t u = u0; u < u1 && ok && !sm.abort_flag; ++seg) {
+                const int64_t end = min(u1, (u / C + 1) * C), first = u;
+                const int buf = seg & 1;
+                if (!mbar_wait_cluster(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u, I8_WAIT_NS)) {
+                    timed_out();
+                    break;
+                }
+                i8_fence_after();
+                for (; u < end; ++u, ++it) {
+                    const int s = it % S;
+                    const uint32_t ph = (uint32_t)(it / S) & 1u;
+                    if (!mbar_wait_cluster(&sm.a_full[s], ph, I8_WAIT_NS) ||
+                        !mbar_wait_bounded(&sm.b_full[s], ph, I8_WAIT_NS)) {
+                        timed_out();
+                        ok = false;
+                        break;
+                    }
+                    i8_fence_after();
+                    const uint32_t a = smem_u32(sm.a[s]), b = smem_u32(sm.b[s]);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        i8_mma<true, 1>(tmem + (uint32_t)(buf * NT), i8_smem_desc(a + kk * 32),
+                                        i8_smem_desc(b + kk * 32), idesc, u > first || kk > 0 ? 1u : 0u);
+                    i8_commit<true>(&sm.empty[s]);
+                }
+                if (ok) i8_commit<true>(&sm.d_full[buf]);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        const int quad = warp & 3;
+        const uint32_t empty_bar[2] = {cluster_addr(&sm.d_empty[0], 0), cluster_addr(&sm.d_empty[1], 0)};
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const int64_t tile = u / C, t0 = tile * C, t1 = t0 + C;
+            const int64_t end = min(u1, t1);
+            const int buf = seg & 1;
+            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u, I8_WAIT_NS);
+            ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
+            if (!ok) {
+                if (lane == 0 && !sm.abort_flag) timed_out();
+                break;
+            }
+            i8_fence_after();
+            const int64_t k = (tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (tile % TM) * NT;
+            const int mc = (int)min((int64_t)NT, p.M - m0);
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NT);
+            const int64_t c0 = i8_run_of(t0, units, G), c1 = i8_run_of(t1 - 1, units, G);
+            auto slot_of = [&](int64_t c) {
+                return p.slots + (((c * 2 + (c == c0 ? 1 : 0)) * 2 + rank) * NT) * 128 + quad * 32 + lane;
+            };
+            bool mine = true;
+            if (c0 != c1) {
+                float* slot = slot_of(pair);
+                for (int c = 0; c < mc; c += 16) {
+                    uint32_t r[16];
+                    i8_tmem_ld16(taddr + (uint32_t)c, r);
+                    i8_tmem_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < mc) slot[(c + i) * 128] = __uint_as_float(r[i]);
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t* counter = p.counters + (c0 * 2 + rank) * 4 + quad;
+                uint32_t old = 0;
+                if (lane == 0) old = atomic_add_acq_rel_gpu(counter, 1u);
+                old = __shfl_sync(0xffffffffu, old, 0);
+                mine = old == (uint32_t)(c1 - c0);
+                if (mine) {
+                    if (lane == 0) *counter = 0u;
+                    __threadfence();
+                }
+            }
+            if (mine) {
+                for (int c = 0; c < mc; c += 16) {
+                    float v[16];
+                    if (c0 == c1) {
+                        uint32_t r[16];
+                        i8_tmem_ld16(taddr + (uint32_t)c, r);
+                        i8_tmem_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+                        for (int64_t o = c0; o <= c1; ++o) {
+                            const float* slot = slot_of(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (c + i < mc) v[i] += __ldcg(slot + (c + i) * 128);
+                        }
+                    }
+                    if (k < p.K) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < mc) p.dx[(m0 + c + i) * p.lddx + k] = (uint16_t)pack_bf16(v[i], 0.f);
+                    }
+                    __syncwarp();
+                }
+            }
+            i8_fence_before();
+            __syncwarp();
+            if (lane == 0) cluster_arrive(empty_bar[buf]);
+            u = end;
+        }
+    } else {
+        // converters: warp w takes rows 32 (w / 4) .. +31; lane (c, g) the
+        // eight rows of block c and the four columns of group (g + 8 c + 8 (w % 4)) % 32
+        const int w = warp - 6, c = lane & 3;
+        const int blk = 4 * (w >> 2) + c, kg = ((lane >> 2) + 8 * c + 8 * (w & 3)) & 31;
+        int it = 0;
+        for (int64_t u = u0; u < u1; ++u, ++it) {
+            const int r = it % R, s = it % S;
+            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.raw_full[r], (uint32_t)(it / R) & 1u, I8_WAIT_NS);
+            ok = ok && mbar_wait_bounded(&sm.empty[s], ((uint32_t)(it / S) & 1u) ^ 1u, I8_WAIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0 && !sm.abort_flag) timed_out();
+                break;
+            }
+            uint32_t in[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                in[i] = *reinterpret_cast<const uint32_t*>(sm.raw[r] + (8 * blk + i) * 128 + 4 * kg);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 4 * kg + j;
+                const uint4 o = make_uint4(i8_pair_bf16(in[0], in[1], j), i8_pair_bf16(in[2], in[3], j),
+                                           i8_pair_bf16(in[4], in[5], j), i8_pair_bf16(in[6], in[7], j));
+                *reinterpret_cast<uint4*>(sm.a[s] + (row >> 3) * 1024 + (row & 7) * 128 +
+                                          ((blk ^ (row & 7)) << 4)) = o;
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");   // to the tensor cores of the pair
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.raw_empty[r]);
+                cluster_arrive(cluster_addr(&sm.a_full[s], 0));
+            }
+        }
+    }
+    __syncthreads();
+    if (sm.abort_flag) {
+        if (warp == 0 && lane == 0) {
+            // the last code copy may be one ahead of the last token copy
+            for (int i = max(0, armed + 1 - R); i < armed + 1; ++i)
+                mbar_wait_bounded(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u, I8_WAIT_NS / 64);
+            if (rank == 0)
+                for (int i = max(0, armed - S); i < armed; ++i)
+                    mbar_wait_bounded(&sm.b_full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
+        }
+        if (warp == 1 && lane == 0 && rank == 0) {
+            i8_commit<true>(&sm.drain);   // every MMA issued so far
+            mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);
+        }
+        __syncwarp();
+        i8_settle();
+    }
+    i8_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        i8_fence_after();
+        i8_tmem_free<true>(tmem, Cfg::COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// g = dy * scale of its channel, rounded to bf16 (the operand above).
+// ---------------------------------------------------------------------------
+template <bool VEC>
+__global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64_t lddy, const float* s, uint16_t* g,
+                                                       int64_t ldg, int M, int N) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int PER = VEC ? 8 : 2;
+    const int cols = (N + PER - 1) / PER;   // g's rows are padded to 64
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)M * cols; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / cols;
+        const int n = (int)(i % cols) * PER;
+        const uint16_t* d = dy + m * lddy + n;
+        float v[PER];
+        if (VEC && n + PER <= N) {
+            const uint4 u = *reinterpret_cast<const uint4*>(d);
+            float f[8];
+            I8Elem<true>::unpack(u, f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] = f[j] * s[n + j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] = n + j < N ? I8Elem<true>::get(d[j]) * s[n + j] : 0.f;
+        }
+        uint32_t* o = reinterpret_cast<uint32_t*>(g + m * ldg + n);
+        if (VEC)
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[PER > 3 ? 3 : 1]),
+                                                      pack_bf16(v[PER > 4 ? 4 : 0], v[PER > 5 ? 5 : 1]),
+                                                      pack_bf16(v[PER > 6 ? 6 : 0], v[PER > 7 ? 7 : 1]));
+        else
+            *o = pack_bf16(v[0], v[1]);
+    }
+}
+
+}  // namespace mpq

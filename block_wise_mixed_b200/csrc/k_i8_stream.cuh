@@ -1,0 +1,316 @@
+// k_i8_stream.cuh -- int8 products for few tokens: the weights' bytes bound
+// the time, so the kernel is a stream of weight tiles through the tensor
+// cores (tcgen05.mma kind::i8).
+//
+//   D[n][m] = sum_k w[n][k] x[m][k]    (128 channels x NT tokens, s32 in TMEM)
+//
+// The channels take the 128 lanes (the wide side of the instruction) and the
+// tokens its columns, so one token costs no more tensor work than NT.  The
+// work is the list of (128-channel tile, 128-byte chunk of k) units, cut into
+// equal contiguous runs, one a CTA and one CTA an SM, whatever the shape: no
+// wave is left half empty and every SM has the same bytes to fetch.  A CTA
+// keeps its whole shared memory in flight as TMA copies.
+// A tile that is cut gets its partial sums through global memory: every
+// contributor writes its own slot, and the last to arrive adds them.  The
+// sums are integers, so the result does not depend on the cuts or the order.
+// Gated: gate and up tiles ride in the same stage, against the same tokens.
+//
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-5 read the
+// accumulators (one TMEM lane quadrant each).  Every wait is bounded.
+#pragma once
+#include "i8_gate.cuh"
+#include "i8_tc.cuh"
+#include "k_i8_rows.cuh"
+
+namespace mpq {
+
+constexpr int I8S_WARPS = 6;
+constexpr int I8S_MAX_CTAS = 256;                     // counters in the workspace
+constexpr int I8_KC = 128;                            // bytes of k in a stage
+
+template <int NT, int NW>
+struct I8StreamCfg {
+    static constexpr int W_BYTES = 128 * I8_KC;
+    static constexpr int X_BYTES = NT * I8_KC;
+    static constexpr int STAGE = NW * W_BYTES + X_BYTES;
+    static constexpr int STAGES = (204 * 1024) / STAGE;
+    static constexpr int BUFS = NW * NT * 2 <= 512 ? 2 : 1;
+    static constexpr uint32_t COLS = NW * NT * BUFS < 32 ? 32 : NW * NT * BUFS;
+};
+
+template <int NT, int NW>
+struct I8StreamSmem {
+    using Cfg = I8StreamCfg<NT, NW>;
+    uint8_t st[Cfg::STAGES][Cfg::STAGE];              // 1024-aligned
+    uint64_t full[Cfg::STAGES], empty[Cfg::STAGES];
+    uint64_t d_full[2], d_empty[2], drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+};
+
+struct I8Product {
+    const float* xs;
+    const float* ws[2];
+    void* y;
+    int64_t ldy;
+    const uint16_t* dh;
+    int64_t lddh;
+    uint16_t* d[2];      // d_gate, d_up (or null)
+    int64_t ldd;
+    uint16_t* g;         // scaled gradients [M][ldg], the up half at + up_off
+    int64_t ldg, up_off;
+    int M, N, K, y_bf16;
+    uint32_t* err;
+    uint32_t* counters;  // zero between calls
+    int32_t* slots;      // partial sums
+};
+
+// What an output element becomes of its sums.  MODE 0: linear, 1: gated,
+// 2: the gradients of gate and up.
+template <int MODE, int ACT>
+__device__ __forceinline__ void i8_finish(const I8Product& p, int64_t m, int64_t n, int acc0, int acc1, float ws0,
+                                          float ws1, float xs, float dh) {
+    const float a = ((float)acc0 * ws0) * xs;
+    if (MODE == 0) {
+        if (p.y_bf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_bf16(a, 0.f);
+        else static_cast<float*>(p.y)[m * p.ldy + n] = a;
+        return;
+    }
+    const float b = ((float)acc1 * ws1) * xs;
+    const Gate g = gate_eval<ACT>(a);
+    if (MODE == 1) {
+        const float h = g.act * b;
+        if (p.y_bf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_bf16(h, 0.f);
+        else static_cast<float*>(p.y)[m * p.ldy + n] = h;
+        return;
+    }
+    const float dg = dh * b * g.grad, du = dh * g.act;
+    if (p.d[0]) {
+        p.d[0][m * p.ldd + n] = (uint16_t)pack_bf16(dg, 0.f);
+        p.d[1][m * p.ldd + n] = (uint16_t)pack_bf16(du, 0.f);
+    }
+    p.g[m * p.ldg + n] = (uint16_t)pack_bf16(dg * ws0, 0.f);
+    p.g[m * p.ldg + p.up_off + n] = (uint16_t)pack_bf16(du * ws1, 0.f);
+}
+
+// Unit u belongs to CTA u * G / units (rounded down the same way as the
+// runs' ends): run c is [c * units / G, (c + 1) * units / G).
+__device__ __forceinline__ int64_t i8_run_start(int64_t c, int64_t units, int64_t G) { return c * units / G; }
+__device__ __forceinline__ int64_t i8_run_of(int64_t u, int64_t units, int64_t G) {
+    return ((u + 1) * G - 1) / units;
+}
+
+template <int NT, int MODE, int ACT>
+__global__ void __launch_bounds__(I8S_WARPS * 32, 1)
+k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap0,
+            const __grid_constant__ CUtensorMap wmap1, I8Product p) {
+    constexpr int NW = MODE == 0 ? 1 : 2;
+    using Cfg = I8StreamCfg<NT, NW>;
+    constexpr int S = Cfg::STAGES, BUFS = Cfg::BUFS;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    I8StreamSmem<NT, NW>& sm = *reinterpret_cast<I8StreamSmem<NT, NW>*>(base);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    const int KB = (p.K + I8_KC - 1) / I8_KC;
+    const int T = (p.N + 127) / 128, TM = (p.M + NT - 1) / NT;
+    const int64_t units = (int64_t)TM * T * KB, G = gridDim.x, cta = blockIdx.x;
+    const int64_t u0 = i8_run_start(cta, units, G), u1 = i8_run_start(cta + 1, units, G);
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.d_full[b], 1);
+            mbar_init(&sm.d_empty[b], 4);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+        i8_tma_prefetch(&xmap);
+        i8_tma_prefetch(&wmap0);
+        if (NW == 2) i8_tma_prefetch(&wmap1);
+    }
+    if (warp == 1) i8_tmem_alloc<false>(&sm.tmem, Cfg::COLS);
+    i8_fence_before();
+    __syncthreads();
+    i8_fence_after();
+    const uint32_t tmem = sm.tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    auto timed_out = [&]() {
+        set_error(p.err, MPQ_ERR_TIMEOUT);
+        sm.abort_flag = 1;
+    };
+    int armed = 0, segs = 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int64_t u = u0; u < u1 && !sm.abort_flag; ++u, ++armed) {
+                const int s = armed % S;
+                if (!mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
+                    timed_out();
+                    break;
+                }
+                const int64_t tile = u / KB;
+                const int kc = (int)(u % KB) * I8_KC, t = (int)(tile % T), mt = (int)(tile / T);
+                mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
+                if (kI8WaitTest) { ++armed; break; }   // armed, no copy
+                const uint32_t bar = smem_u32(&sm.full[s]);
+                i8_tma_load<false>(sm.st[s], &wmap0, kc, t * 128, bar);
+                if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, t * 128, bar);
+                i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, mt * NT, bar);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = i8_idesc(128, NT);
+            int it = 0;
+            for (int64_t u = u0; u < u1 && !sm.abort_flag;) {
+                const int64_t end = min(u1, (u / KB + 1) * KB);
+                const int buf = segs % BUFS;
+                if (!mbar_wait_bounded(&sm.d_empty[buf], ((uint32_t)(segs / BUFS) & 1u) ^ 1u, I8_WAIT_NS)) {
+                    timed_out();
+                    break;
+                }
+                i8_fence_after();
+                const int64_t first = u;
+                bool ok = true;
+                for (; u < end; ++u, ++it) {
+                    const int s = it % S;
+                    if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(it / S) & 1u, I8_WAIT_NS)) {
+                        timed_out();
+                        ok = false;
+                        break;
+                    }
+                    i8_fence_after();
+                    const uint32_t st = smem_u32(sm.st[s]);
+#pragma unroll
+                    for (int j = 0; j < NW; ++j)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            i8_mma<false, 0>(tmem + (uint32_t)((buf * NW + j) * NT),
+                                             i8_smem_desc(st + j * Cfg::W_BYTES + kk * 32),
+                                             i8_smem_desc(st + NW * Cfg::W_BYTES + kk * 32), idesc,
+                                             u > first || kk > 0 ? 1u : 0u);
+                    i8_commit<false>(&sm.empty[s]);
+                }
+                if (!ok) break;
+                i8_commit<false>(&sm.d_full[buf]);
+                ++segs;
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const int64_t tile = u / KB, t0 = tile * KB, t1 = t0 + KB;
+            const int64_t end = min(u1, t1);
+            const int buf = seg % BUFS;
+            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.d_full[buf], (uint32_t)(seg / BUFS) & 1u, I8_WAIT_NS);
+            ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
+            if (!ok) {
+                if (lane == 0 && !sm.abort_flag) timed_out();
+                break;
+            }
+            i8_fence_after();
+            const int n = (int)(tile % T) * 128 + quad * 32 + lane, m0 = (int)(tile / T) * NT;
+            const int mc = min(NT, p.M - m0);
+            const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NW * NT);
+            const bool in = n < p.N;
+            const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
+            // contributors c0 .. c1; this CTA's slot: 1 for the tile that
+            // starts inside its run, 0 for the one that began before it
+            const int64_t c0 = i8_run_of(t0, units, G), c1 = i8_run_of(t1 - 1, units, G);
+            auto slot_of = [&](int64_t c) {
+                return p.slots + ((c * 2 + (c == c0 ? 1 : 0)) * NW * NT) * 128 + quad * 32 + lane;
+            };
+            bool mine = true;   // this warp writes the results
+            if (c0 != c1) {
+                int32_t* slot = slot_of(cta);
+                for (int c = 0; c < mc; c += 16) {
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint32_t r[16];
+                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
+                        i8_tmem_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[i];
+                    }
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t old = 0;
+                if (lane == 0) old = atomic_add_acq_rel_gpu(&p.counters[c0 * 4 + quad], 1u);
+                old = __shfl_sync(0xffffffffu, old, 0);
+                mine = old == (uint32_t)(c1 - c0);
+                if (mine) {
+                    if (lane == 0) p.counters[c0 * 4 + quad] = 0u;   // clean for the next call
+                    __threadfence();
+                }
+            }
+            if (mine) {
+                for (int c = 0; c < mc; c += 16) {
+                    int acc[NW][16];
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint32_t r[16];
+                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
+                        i8_tmem_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[j][i] = (int)r[i];
+                    }
+                    for (int64_t o = c0; o <= c1; ++o) {
+                        if (c0 == c1 || o == cta) continue;
+                        const int32_t* slot = slot_of(o);
+#pragma unroll
+                        for (int j = 0; j < NW; ++j)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (c + i < mc) acc[j][i] += __ldcg(slot + (j * NT + c + i) * 128);
+                    }
+                    if (in) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < mc) {
+                                const int64_t m = m0 + c + i;
+                                const float dh = MODE == 2 ? I8Elem<true>::get(p.dh[m * p.lddh + n]) : 0.f;
+                                i8_finish<MODE, ACT>(p, m, n, acc[0][i], acc[NW - 1][i], ws0, ws1, p.xs[m], dh);
+                            }
+                    }
+                    __syncwarp();
+                }
+            }
+            i8_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.d_empty[buf]);
+            u = end;
+        }
+    }
+    // copies and MMAs in flight land before shared memory and TMEM are given
+    // up (after an abort they may be; else this is already so)
+    __syncthreads();
+    if (sm.abort_flag && lane == 0) {
+        if (warp == 0)
+            for (int i = max(0, armed - S); i < armed; ++i)
+                mbar_wait_bounded(&sm.full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
+        if (warp == 1) {
+            i8_commit<false>(&sm.drain);   // every MMA issued so far
+            mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);
+        }
+    }
+    i8_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        i8_fence_after();
+        i8_tmem_free<false>(tmem, Cfg::COLS);
+    }
+}
+
+}  // namespace mpq

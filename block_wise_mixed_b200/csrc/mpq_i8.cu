@@ -1,16 +1,20 @@
 // mpq_i8.cu -- the C ABI of the 8-bit integer operators (include/mpq.h):
 // argument checks, workspace layout and launches.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/mpq.h"
 #include "common.cuh"
 #include "i8_gate.cuh"
+#include "k_i8_dx.cuh"
 #include "k_i8_rows.cuh"
-#include "k_i8_simple.cuh"
+#include "k_i8_stream.cuh"
+#include "k_i8_tile.cuh"
 
 using namespace mpq;
 
@@ -23,7 +27,7 @@ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 mpq_status check_i8(const mpq_i8* q) {
     if (!q) return MPQ_ERR_ARG;
     if (q->rows < 0 || q->cols < 1 || q->cols > MPQ_I8_MAX_COLS) return MPQ_ERR_SHAPE;
-    if (q->ld < q->cols || q->ld % 16 != 0) return MPQ_ERR_ARG;
+    if (q->ld < q->cols || q->ld % 16 != 0 || q->ld >= ((int64_t)1 << 40)) return MPQ_ERR_ARG;
     if (q->rows == 0) return MPQ_OK;
     if (!q->codes || !q->scales || !aligned(q->codes, 16) || !aligned(q->scales, 4)) return MPQ_ERR_ARG;
     return MPQ_OK;
@@ -133,20 +137,70 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
 
 namespace {
 
+constexpr int kSMs = 148;
+constexpr int kPairs = kSMs / 2;
+// Up to here the weights' bytes bound a product and k_i8_stream takes it;
+// above, k_i8_tile.
+constexpr int kStreamMaxM = 128;
+
 // Workspace: the error word, the counters (zero between calls), then scratch
 // that a call writes before it reads.  The zeroed part has one size for all
 // mpq_i8_* calls, so one workspace serves them all, one after another.
-constexpr size_t kI8ZeroBytes = 256;
+constexpr size_t kErrBytes = 256;
+constexpr size_t kI8ZeroBytes = kErrBytes + (size_t)kSMs * 4 * 4 + 256 - (size_t)kSMs * 4 * 4 % 256;
 
 inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
 }
 
+// Tokens per tile of the streaming kernel, and of the gradient kernel.
+inline int stream_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K) {
+    return std::min<int64_t>(kSMs, div_up(M, stream_nt(M)) * div_up(N, 128) * div_up(K, I8_KC));
+}
+inline int64_t dx_pairs(int64_t M, int64_t N, int64_t K, int nw) {
+    return std::min<int64_t>(kPairs, div_up(M, dx_nt(M)) * div_up(K, 256) * div_up(N, I8X_NC) * nw);
+}
+
+// Partial sums: two slots a CTA (or pair), 128 lanes x NT columns each.
+inline size_t product_slots(int64_t M, int64_t N, int64_t K, int nw) {
+    return M > kStreamMaxM ? 0 : (size_t)stream_ctas(M, N, K) * 2 * nw * stream_nt(M) * 128 * 4;
+}
+inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
+    return (size_t)dx_pairs(M, N, K, nw) * 2 * 2 * dx_nt(M) * 128 * 4;
+}
+
 inline int64_t grad_ld(int64_t n) { return div_up(n, 64) * 64; }
 
-inline size_t i8_ws_bytes(int64_t M, int64_t N, int64_t K, int grads) {
-    if (!shape_ok(M, N, K)) return 0;
-    return round256(kI8ZeroBytes + (size_t)M * (size_t)grad_ld(N) * 2 * (size_t)grads);
+struct I8Ws {
+    uint32_t* err;
+    uint32_t* counters;
+    void* slots;
+    uint16_t* grads;
+    size_t bytes;
+};
+I8Ws carve(void* ws, size_t slots, size_t grads) {
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    I8Ws w{};
+    const size_t after = kI8ZeroBytes + round256(slots);
+    w.bytes = after + round256(grads);
+    if (!b) return w;
+    w.err = reinterpret_cast<uint32_t*>(b);
+    w.counters = reinterpret_cast<uint32_t*>(b + kErrBytes);
+    w.slots = b + kI8ZeroBytes;
+    w.grads = reinterpret_cast<uint16_t*>(b + after);
+    return w;
+}
+
+I8Ws ws_product(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
+    return carve(ws, product_slots(M, N, K, nw), 0);
+}
+// nw matrices: the product's slots (gated) and the gradient's share their place.
+I8Ws ws_backward(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
+    const size_t ps = nw == 2 ? product_slots(M, N, K, 2) : 0;
+    return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * (size_t)grad_ld(N) * 2 * (size_t)nw);
 }
 
 // x and the weights of a product: common columns, at least one channel.
@@ -161,44 +215,144 @@ mpq_status check_product(const mpq_i8* x, const mpq_i8* const* w, int nw) {
     return MPQ_OK;
 }
 
-I8GemmParams gemm_params(const mpq_i8* x, const mpq_i8* const* w, int nw) {
-    I8GemmParams p{};
-    p.x = x->codes;
-    p.xs = x->scales;
-    p.ldx = x->ld;
-    for (int i = 0; i < nw; ++i) {
-        p.w[i] = w[i]->codes;
-        p.ws[i] = w[i]->scales;
-        p.ldw[i] = w[i]->ld;
+// ---------------------------------------------------------------------------
+// tensor maps
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// rows x cols elements, ld bytes a row, boxes of box_rows x 128 bytes; what
+// lies outside reads as zero.
+bool make_map(CUtensorMap* map, const void* ptr, bool bf16, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+              bool swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1u, 1u};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_map(CUtensorMap* map, const mpq_i8* q, int box_rows, bool swizzle) {
+    return make_map(map, q->codes, false, q->rows, q->cols, q->ld, box_rows, swizzle);
+}
+
+// Launches with all the shared memory a kernel asks for (raised once per device).
+template <auto Kernel, typename... Args>
+mpq_status launch_big(dim3 grid, int threads, size_t smem, void* stream, Args&&... args) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MPQ_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return MPQ_ERR_CUDA;
+        done.fetch_or(bit, std::memory_order_acq_rel);
     }
+    return launch(Kernel, grid, threads, smem, stream, std::forward<Args>(args)...);
+}
+
+template <int NT, int MODE, int ACT>
+mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& p, void* stream) {
+    constexpr int NW = MODE == 0 ? 1 : 2;
+    CUtensorMap xm, w0, w1;
+    if (!make_map(&xm, x, NT, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
+        return MPQ_ERR_CUDA;
+    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)stream_ctas(p.M, p.N, p.K)), I8S_WARPS * 32,
+                                                  sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p);
+}
+
+template <int MODE, int ACT>
+mpq_status tile_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& p, void* stream) {
+    constexpr int NW = MODE == 0 ? 1 : 2;
+    CUtensorMap xm, w0, w1;
+    if (!make_map(&xm, x, 128, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
+        return MPQ_ERR_CUDA;
+    const int64_t tiles = div_up(p.M, 256) * div_up(p.N, 256 / NW);
+    return launch_big<k_i8_tile<MODE, ACT>>(dim3((unsigned)(2 * std::min<int64_t>(kPairs, tiles))), I8T_WARPS * 32,
+                                            sizeof(I8TileSmem<MODE>) + 1024, stream, xm, w0, w1, p);
+}
+
+template <int MODE, int ACT>
+mpq_status product_run(const mpq_i8* x, const mpq_i8* const* w, I8Product& p, const I8Ws& ws, void* stream) {
+    p.xs = x->scales;
+    p.ws[0] = w[0]->scales;
+    p.ws[1] = MODE == 0 ? nullptr : w[1]->scales;
     p.M = x->rows;
     p.N = w[0]->rows;
     p.K = x->cols;
-    return p;
+    p.err = ws.err;
+    p.counters = ws.counters;
+    p.slots = static_cast<int32_t*>(ws.slots);
+    if (p.M > kStreamMaxM) return tile_run<MODE, ACT>(x, w, p, stream);
+    switch (stream_nt(p.M)) {
+        case 16: return stream_run<16, MODE, ACT>(x, w, p, stream);
+        case 32: return stream_run<32, MODE, ACT>(x, w, p, stream);
+        case 64: return stream_run<64, MODE, ACT>(x, w, p, stream);
+        default: return stream_run<128, MODE, ACT>(x, w, p, stream);
+    }
 }
 
-template <int MODE>
-mpq_status gemm_run(const I8GemmParams& p, mpq_act act, void* stream) {
-    const dim3 grid((unsigned)div_up(p.N, 64), (unsigned)div_up(p.M, 64));
-    if (grid.y > 65535) return MPQ_ERR_SHAPE;
-    return act == MPQ_ACT_SILU ? launch(k_i8_simple<MODE, MPQ_ACT_SILU>, grid, 256, 0, stream, p)
-                               : launch(k_i8_simple<MODE, MPQ_ACT_GELU_TANH>, grid, 256, 0, stream, p);
+template <int NT>
+mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, I8DxParams& p,
+                  void* stream) {
+    CUtensorMap w0, w1, g0, g1;
+    if (!make_map(&w0, w[0], I8X_NC, false) || !make_map(&w1, w[nw - 1], I8X_NC, false) ||
+        !make_map(&g0, g, true, p.M, p.N, ldg * 2, NT / 2, true) ||
+        !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
+        return MPQ_ERR_CUDA;
+    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * dx_pairs(p.M, p.N, p.K, nw))), I8X_WARPS * 32,
+                                   sizeof(I8DxSmem<NT>) + 1024, stream, w0, w1, g0, g1, p);
 }
 
-mpq_status dx_run(const I8DxParams& p, void* stream) {
-    const dim3 grid((unsigned)div_up(p.K, 64), (unsigned)div_up(p.M, 64));
-    if (grid.y > 65535) return MPQ_ERR_SHAPE;
-    return launch(k_i8_dx_simple, grid, 256, 0, stream, p);
+mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, int64_t M,
+                  void* dx_dev, int64_t lddx, const I8Ws& ws, void* stream) {
+    I8DxParams p{};
+    p.dx = static_cast<uint16_t*>(dx_dev);
+    p.lddx = lddx;
+    p.M = (int)M;
+    p.N = w[0]->rows;
+    p.K = w[0]->cols;
+    p.nw = nw;
+    p.err = ws.err;
+    p.counters = ws.counters;
+    p.slots = static_cast<float*>(ws.slots);
+    switch (dx_nt(M)) {
+        case 32: return dx_run<32>(w, nw, g, ldg, up_off, p, stream);
+        case 64: return dx_run<64>(w, nw, g, ldg, up_off, p, stream);
+        case 128: return dx_run<128>(w, nw, g, ldg, up_off, p, stream);
+        default: return dx_run<256>(w, nw, g, ldg, up_off, p, stream);
+    }
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t mpq_i8_linear_workspace_size(int32_t M, int32_t N, int32_t K) { return i8_ws_bytes(M, N, K, 0); }
-size_t mpq_i8_gated_workspace_size(int32_t M, int32_t F, int32_t K) { return i8_ws_bytes(M, F, K, 0); }
-size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K) { return i8_ws_bytes(M, N, K, 1); }
-size_t mpq_i8_gated_backward_workspace_size(int32_t M, int32_t F, int32_t K) { return i8_ws_bytes(M, F, K, 2); }
+size_t mpq_i8_linear_workspace_size(int32_t M, int32_t N, int32_t K) {
+    return shape_ok(M, N, K) ? ws_product(nullptr, M, N, K, 1).bytes : 0;
+}
+size_t mpq_i8_gated_workspace_size(int32_t M, int32_t F, int32_t K) {
+    return shape_ok(M, F, K) ? ws_product(nullptr, M, F, K, 2).bytes : 0;
+}
+size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K) {
+    return shape_ok(M, N, K) ? ws_backward(nullptr, M, N, K, 1).bytes : 0;
+}
+size_t mpq_i8_gated_backward_workspace_size(int32_t M, int32_t F, int32_t K) {
+    return shape_ok(M, F, K) ? ws_backward(nullptr, M, F, K, 2).bytes : 0;
+}
 
 mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydtype ydt, int64_t ldy, void* ws,
                          size_t ws_bytes, void* stream) {
@@ -207,14 +361,15 @@ mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydty
     if (st != MPQ_OK) return st;
     if (!dtype_ok(ydt)) return MPQ_ERR_ARG;
     if (x->rows == 0) return MPQ_OK;
+    const I8Ws k = ws_product(ws, x->rows, w->rows, x->cols, 1);
     st = check_array(y_dev, elem_size(ydt), ldy, w->rows);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, mpq_i8_linear_workspace_size(x->rows, w->rows, x->cols));
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
     if (st != MPQ_OK) return st;
-    I8GemmParams p = gemm_params(x, wl, 1);
+    I8Product p{};
     p.y = y_dev;
     p.ldy = ldy;
     p.y_bf16 = ydt == MPQ_Y_BF16;
-    return gemm_run<0>(p, MPQ_ACT_SILU, stream);
+    return product_run<0, MPQ_ACT_SILU>(x, wl, p, k, stream);
 }
 
 mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_up, mpq_act act, void* h_dev,
@@ -224,14 +379,16 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
     if (st != MPQ_OK) return st;
     if (!dtype_ok(ydt) || !act_ok(act)) return MPQ_ERR_ARG;
     if (x->rows == 0) return MPQ_OK;
+    const I8Ws k = ws_product(ws, x->rows, w_gate->rows, x->cols, 2);
     st = check_array(h_dev, elem_size(ydt), ldh, w_gate->rows);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, mpq_i8_gated_workspace_size(x->rows, w_gate->rows, x->cols));
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
     if (st != MPQ_OK) return st;
-    I8GemmParams p = gemm_params(x, wl, 2);
+    I8Product p{};
     p.y = h_dev;
     p.ldy = ldh;
     p.y_bf16 = ydt == MPQ_Y_BF16;
-    return gemm_run<1>(p, act, stream);
+    return act == MPQ_ACT_SILU ? product_run<1, MPQ_ACT_SILU>(x, wl, p, k, stream)
+                               : product_run<1, MPQ_ACT_GELU_TANH>(x, wl, p, k, stream);
 }
 
 mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M, int64_t lddy, void* dx_dev,
@@ -240,28 +397,20 @@ mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M
     if (st != MPQ_OK) return st;
     if (M < 0 || w->rows < 1) return MPQ_ERR_SHAPE;
     if (M == 0) return MPQ_OK;
+    const I8Ws k = ws_backward(ws, M, w->rows, w->cols, 1);
     st = check_array(dy_dev, 2, lddy, w->rows);
     if (st == MPQ_OK) st = check_array(dx_dev, 2, lddx, w->cols);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, mpq_i8_linear_backward_workspace_size(M, w->rows, w->cols));
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
     if (st != MPQ_OK) return st;
-    uint16_t* g = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kI8ZeroBytes);
     const int64_t ldg = grad_ld(w->rows);
-    const unsigned blocks = (unsigned)std::min<int64_t>(div_up((int64_t)M * w->rows, 256), 148 * 8);
-    st = launch(k_i8_scale_grad, dim3(blocks), 256, 0, stream, static_cast<const uint16_t*>(dy_dev), lddy, w->scales,
-                g, ldg, M, w->rows);
+    const bool vec = aligned(dy_dev, 16) && (M == 1 || lddy % 8 == 0);
+    const unsigned blocks = (unsigned)std::min<int64_t>(div_up((int64_t)M * ldg / (vec ? 8 : 2), 256), kSMs * 8);
+    const uint16_t* dy = static_cast<const uint16_t*>(dy_dev);
+    st = vec ? launch(k_i8_scale_grad<true>, dim3(blocks), 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows)
+             : launch(k_i8_scale_grad<false>, dim3(blocks), 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M,
+                      w->rows);
     if (st != MPQ_OK) return st;
-    I8DxParams d{};
-    d.g = g;
-    d.ldg = ldg;
-    d.w[0] = w->codes;
-    d.ldw[0] = w->ld;
-    d.dx = static_cast<uint16_t*>(dx_dev);
-    d.lddx = lddx;
-    d.M = M;
-    d.N = w->rows;
-    d.K = w->cols;
-    d.nw = 1;
-    return dx_run(d, stream);
+    return dx_run(&w, 1, k.grads, ldg, 0, M, dx_dev, lddx, k, stream);
 }
 
 mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_up, mpq_act act,
@@ -273,38 +422,26 @@ mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mp
     if (!act_ok(act) || (d_gate_dev == nullptr) != (d_up_dev == nullptr)) return MPQ_ERR_ARG;
     if (x->rows == 0) return MPQ_OK;
     const int64_t F = w_gate->rows;
+    const I8Ws k = ws_backward(ws, x->rows, F, x->cols, 2);
     st = check_array(dh_dev, 2, lddh, F);
     if (st == MPQ_OK && d_gate_dev) st = check_array(d_gate_dev, 2, ldd, F);
     if (st == MPQ_OK && d_up_dev) st = check_array(d_up_dev, 2, ldd, F);
     if (st == MPQ_OK) st = check_array(dx_dev, 2, lddx, x->cols);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, mpq_i8_gated_backward_workspace_size(x->rows, (int32_t)F, x->cols));
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
     if (st != MPQ_OK) return st;
-    I8GemmParams p = gemm_params(x, wl, 2);
+    I8Product p{};
     p.dh = static_cast<const uint16_t*>(dh_dev);
     p.lddh = lddh;
     p.d[0] = static_cast<uint16_t*>(d_gate_dev);
     p.d[1] = static_cast<uint16_t*>(d_up_dev);
     p.ldd = ldd;
-    p.g = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kI8ZeroBytes);
+    p.g = k.grads;
     p.up_off = grad_ld(F);
     p.ldg = 2 * p.up_off;
-    st = gemm_run<2>(p, act, stream);
+    st = act == MPQ_ACT_SILU ? product_run<2, MPQ_ACT_SILU>(x, wl, p, k, stream)
+                             : product_run<2, MPQ_ACT_GELU_TANH>(x, wl, p, k, stream);
     if (st != MPQ_OK) return st;
-    I8DxParams d{};
-    d.g = p.g;
-    d.ldg = p.ldg;
-    d.up_off = p.up_off;
-    d.w[0] = w_gate->codes;
-    d.w[1] = w_up->codes;
-    d.ldw[0] = w_gate->ld;
-    d.ldw[1] = w_up->ld;
-    d.dx = static_cast<uint16_t*>(dx_dev);
-    d.lddx = lddx;
-    d.M = x->rows;
-    d.N = (int)F;
-    d.K = x->cols;
-    d.nw = 2;
-    return dx_run(d, stream);
+    return dx_run(wl, 2, k.grads, p.ldg, p.up_off, x->rows, dx_dev, lddx, k, stream);
 }
 
 }  // extern "C"
