@@ -8,7 +8,7 @@
 // tokens over the two SMs of a cluster.
 //
 // The codes lie with k along the rows and the contraction across them; the
-// operand wants the contraction along its rows, in bf16.  Eight warps turn
+// operand wants the contraction along its rows, in bf16.  Sixteen warps turn
 // each 64 x 128 code tile (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
 // one byte permute, and makes them bf16 with two masks and one subtraction:
@@ -30,8 +30,9 @@
 
 namespace mpq {
 
-constexpr int I8X_CONV = 8;
-constexpr int I8X_WARPS = 6 + I8X_CONV;
+constexpr int I8X_GROUPS = 4;               // converter groups, a stage each in turn
+constexpr int I8X_GWARPS = 4;               // warps of a group
+constexpr int I8X_WARPS = 6 + I8X_GROUPS * I8X_GWARPS;
 constexpr int I8X_NC = 64;                  // channels in a stage
 constexpr int I8X_RAW = I8X_NC * 128;       // codes of a stage
 constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
@@ -95,10 +96,10 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     if (tid == 0) {
         for (int s = 0; s < R; ++s) {
             mbar_init(&sm.raw_full[s], 1);
-            mbar_init(&sm.raw_empty[s], I8X_CONV);
+            mbar_init(&sm.raw_empty[s], I8X_GWARPS);
         }
         for (int s = 0; s < S; ++s) {
-            mbar_init(&sm.a_full[s], 2 * I8X_CONV);
+            mbar_init(&sm.a_full[s], 2 * I8X_GWARPS);
             mbar_init(&sm.b_full[s], 1);
             mbar_init(&sm.empty[s], 1);
         }
@@ -241,27 +242,39 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 }
             }
             if (mine) {
-                for (int c = 0; c < mc; c += 16) {
-                    float v[16];
+                for (int c = 0; c < mc; c += 8) {
+                    float v[8];
                     if (c0 == c1) {
-                        uint32_t r[16];
-                        i8_tmem_ld16(taddr + (uint32_t)c, r);
+                        uint32_t r[8];
+                        i8_tmem_ld8(taddr + (uint32_t)c, r);
                         i8_tmem_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-                        for (int64_t o = c0; o <= c1; ++o) {
-                            const float* slot = slot_of(o);
+                        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                        // in the order of the runs; four contributors' loads
+                        // in flight at a time
+                        for (int64_t o = c0; o <= c1; o += 4) {
+                            float t[4][8];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (c + i < mc) v[i] += __ldcg(slot + (c + i) * 128);
+                            for (int q = 0; q < 4; ++q)
+                                if (o + q <= c1) {
+                                    const float* slot = slot_of(o + q);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        if (c + i < mc) t[q][i] = __ldcg(slot + (c + i) * 128);
+                                }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (o + q <= c1)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) v[i] += t[q][i];
                         }
                     }
                     if (k < p.K) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < 8; ++i)
                             if (c + i < mc) p.dx[(m0 + c + i) * p.lddx + k] = (uint16_t)pack_bf16(v[i], 0.f);
                     }
                     __syncwarp();
@@ -273,13 +286,16 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             u = end;
         }
     } else {
-        // converters: warp w takes rows 32 (w / 4) .. +31; lane (c, g) the
-        // eight rows of block c and the four columns of group (g + 8 c + 8 (w % 4)) % 32
-        const int w = warp - 6, c = lane & 3;
-        const int blk = 4 * (w >> 2) + c, kg = ((lane >> 2) + 8 * c + 8 * (w & 3)) & 31;
-        int it = 0;
-        for (int64_t u = u0; u < u1; ++u, ++it) {
-            const int r = it % R, s = it % S;
+        // converters: a group takes every fourth stage, so that four stages'
+        // waits, loads and fences overlap.  Warp q of it takes rows 0 .. 31,
+        // then 32 .. 63; lane (c, g) the eight rows of block c and the four
+        // columns of group (g + 8 c + 8 q) % 32
+        const int group = (warp - 6) / I8X_GWARPS, q = (warp - 6) % I8X_GWARPS, c = lane & 3;
+        const int kg = ((lane >> 2) + 8 * c + 8 * q) & 31;
+        const uint32_t row0 = (uint32_t)(4 * kg);
+        const int64_t n_units = u1 - u0;
+        for (int64_t it = group; it < n_units; it += I8X_GROUPS) {
+            const int r = (int)(it % R), s = (int)(it % S);
             bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.raw_full[r], (uint32_t)(it / R) & 1u, I8_WAIT_NS);
             ok = ok && mbar_wait_bounded(&sm.empty[s], ((uint32_t)(it / S) & 1u) ^ 1u, I8_WAIT_NS);
             ok = __all_sync(0xffffffffu, ok);
@@ -287,19 +303,23 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 if (lane == 0 && !sm.abort_flag) timed_out();
                 break;
             }
-            uint32_t in[8];
+            uint32_t in[2][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                in[i] = *reinterpret_cast<const uint32_t*>(sm.raw[r] + (8 * blk + i) * 128 + 4 * kg);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 4 * kg + j;
-                const uint4 o = make_uint4(i8_pair_bf16(in[0], in[1], j), i8_pair_bf16(in[2], in[3], j),
-                                           i8_pair_bf16(in[4], in[5], j), i8_pair_bf16(in[6], in[7], j));
-                *reinterpret_cast<uint4*>(sm.a[s] + (row >> 3) * 1024 + (row & 7) * 128 +
-                                          ((blk ^ (row & 7)) << 4)) = o;
-            }
-            asm volatile("fence.proxy.async;" ::: "memory");   // to the tensor cores of the pair
+                for (int i = 0; i < 8; ++i)
+                    in[h][i] = *reinterpret_cast<const uint32_t*>(sm.raw[r] + (32 * h + 8 * c + i) * 128 + 4 * kg);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t row = row0 + j;
+                    const uint4 o = make_uint4(i8_pair_bf16(in[h][0], in[h][1], j), i8_pair_bf16(in[h][2], in[h][3], j),
+                                               i8_pair_bf16(in[h][4], in[h][5], j), i8_pair_bf16(in[h][6], in[h][7], j));
+                    *reinterpret_cast<uint4*>(sm.a[s] + (row >> 3) * 1024 + (row & 7) * 128 +
+                                              (((4 * h + c) ^ (row & 7)) << 4)) = o;
+                }
+            fence_proxy_async_smem();   // to the tensor cores
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.raw_empty[r]);

@@ -266,15 +266,26 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[j][i] = (int)r[i];
                     }
-                    for (int64_t o = c0; o <= c1; ++o) {
-                        if (c0 == c1 || o == cta) continue;
-                        const int32_t* slot = slot_of(o);
+                    if (c0 != c1)
+                        for (int64_t o = c0; o <= c1; o += 2) {   // two contributors' loads in flight
+                            int t[2][NW][16];
 #pragma unroll
-                        for (int j = 0; j < NW; ++j)
+                            for (int q = 0; q < 2; ++q) {
+                                const bool add = o + q <= c1 && o + q != cta;
+                                const int32_t* slot = slot_of(o + q);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (c + i < mc) acc[j][i] += __ldcg(slot + (j * NT + c + i) * 128);
-                    }
+                                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        t[q][j][i] = add && c + i < mc ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
+                            }
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) acc[j][i] += t[q][j][i];
+                        }
                     if (in) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/mpq.h"
@@ -157,16 +158,25 @@ inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
 inline int stream_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
-inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K) {
-    return std::min<int64_t>(kSMs, div_up(M, stream_nt(M)) * div_up(N, 128) * div_up(K, I8_KC));
+// Runs that a tile of `chunks` units may be cut into: a unit costs about as
+// long (0.35 us at an SM's share of HBM) as the last contributor takes to add
+// 14 columns of one more partial sum, so n runs cost chunks / n + n cols / 14
+// units, least at n = sqrt(14 chunks / cols).
+inline int64_t max_cuts(int64_t chunks, int64_t cols) {
+    return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(14.0 * (double)chunks / (double)cols)));
+}
+inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K, int nw) {
+    const int64_t chunks = div_up(K, I8_KC), tiles = div_up(M, stream_nt(M)) * div_up(N, 128);
+    return std::min<int64_t>({(int64_t)kSMs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, stream_nt(M)) * nw)});
 }
 inline int64_t dx_pairs(int64_t M, int64_t N, int64_t K, int nw) {
-    return std::min<int64_t>(kPairs, div_up(M, dx_nt(M)) * div_up(K, 256) * div_up(N, I8X_NC) * nw);
+    const int64_t chunks = div_up(N, I8X_NC) * nw, tiles = div_up(M, dx_nt(M)) * div_up(K, 256);
+    return std::min<int64_t>({(int64_t)kPairs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, dx_nt(M)))});
 }
 
 // Partial sums: two slots a CTA (or pair), 128 lanes x NT columns each.
 inline size_t product_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    return M > kStreamMaxM ? 0 : (size_t)stream_ctas(M, N, K) * 2 * nw * stream_nt(M) * 128 * 4;
+    return M > kStreamMaxM ? 0 : (size_t)stream_ctas(M, N, K, nw) * 2 * nw * stream_nt(M) * 128 * 4;
 }
 inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
     return (size_t)dx_pairs(M, N, K, nw) * 2 * 2 * dx_nt(M) * 128 * 4;
@@ -270,7 +280,7 @@ mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& 
     CUtensorMap xm, w0, w1;
     if (!make_map(&xm, x, NT, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
         return MPQ_ERR_CUDA;
-    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)stream_ctas(p.M, p.N, p.K)), I8S_WARPS * 32,
+    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)stream_ctas(p.M, p.N, p.K, NW)), I8S_WARPS * 32,
                                                   sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p);
 }
 
