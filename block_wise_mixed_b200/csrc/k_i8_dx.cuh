@@ -32,7 +32,7 @@ namespace mpq {
 
 constexpr int I8X_GROUPS = 4;               // converter groups, a stage each in turn
 constexpr int I8X_GWARPS = 4;               // warps of a group
-constexpr int I8X_WARPS = 6 + I8X_GROUPS * I8X_GWARPS;
+constexpr int I8X_WARPS = 7 + I8X_GROUPS * I8X_GWARPS;
 constexpr int I8X_NC = 64;                  // channels in a stage
 constexpr int I8X_RAW = I8X_NC * 128;       // codes of a stage
 constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
@@ -40,8 +40,8 @@ constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
 template <int NT>
 struct I8DxCfg {
     static constexpr int B = NT / 2 * I8X_NC * 2;              // this CTA's tokens
-    static constexpr int R = 6;                                // code stages
-    static constexpr int S = NT == 256 ? 5 : 6;                // operand stages
+    static constexpr int S = NT == 256 ? 5 : NT == 128 ? 6 : 8;        // operand stages
+    static constexpr int R = NT == 256 ? 6 : 8;                        // code stages
     static constexpr uint32_t COLS = 2 * NT;                   // double-buffered accumulator
 };
 
@@ -67,6 +67,29 @@ struct I8DxParams {
     float* slots;
 };
 
+// Where a unit lies: tile (tk, tm), matrix j and its channel block n; counted
+// along, since a 64-bit division a unit would hold the copies up.
+struct I8DxPlace {
+    int tk, tm, j, n;
+    __device__ __forceinline__ I8DxPlace(int64_t u, int C, int NB, int64_t TM) {
+        const int64_t tile = u / C;
+        const int c = (int)(u - tile * C);
+        tk = (int)(tile / TM);
+        tm = (int)(tile % TM);
+        j = c / NB;
+        n = c - j * NB;
+    }
+    __device__ __forceinline__ void next(int C, int NB, int64_t TM) {
+        if (++n < NB) return;
+        n = 0;
+        if (++j * NB < C) return;
+        j = 0;
+        if (++tm < TM) return;
+        tm = 0;
+        ++tk;
+    }
+};
+
 // Bytes j of two rows' words as a pair of bf16 values.
 __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j) {
     const uint32_t t = __byte_perm(wa, wb, (uint32_t)(j | (j << 4) | ((4 + j) << 8) | ((4 + j) << 12)));
@@ -82,6 +105,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p) {
     using Cfg = I8DxCfg<NT>;
     constexpr int S = Cfg::S, R = Cfg::R;
+    static_assert(R >= S && S >= I8X_GROUPS, "the converters' parity waits");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     I8DxSmem<NT>& sm = *reinterpret_cast<I8DxSmem<NT>*>(base);
@@ -126,35 +150,42 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         set_error(p.err, MPQ_ERR_TIMEOUT);
         sm.abort_flag = 1;
     };
-    int armed = 0;   // units whose copies were issued
+    int armed = 0;   // units whose copies were issued (warp 0: codes, the last warp: tokens)
 
     if (warp == 0) {
         if (lane == 0) {
-            for (int64_t u = u0; u < u1; ++u) {
-                const int64_t tile = u / C;
-                const int c = (int)(u % C), j = c / NB, n = (c % NB) * I8X_NC;
-                const int k0 = (int)(tile / TM) * 256 + (int)rank * 128;
-                const int m0 = (int)((tile % TM) * NT + rank * (NT / 2));
-                const int r = armed % R, s = armed % S;
-                bool ok = !sm.abort_flag &&
-                          mbar_wait_bounded(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u, I8_WAIT_NS);
-                if (!ok) {
+            I8DxPlace at(u0, C, NB, TM);
+            for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
+                const int k0 = at.tk * 256 + (int)rank * 128;
+                const int r = armed % R;
+                if (sm.abort_flag || !mbar_wait_bounded(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u, I8_WAIT_NS)) {
                     if (!sm.abort_flag) timed_out();
                     break;
                 }
                 mbar_arrive_expect_tx(&sm.raw_full[r], I8X_RAW);
+                ++armed;
                 if (kI8WaitTest) break;   // armed, no copy
-                i8_tma_load<false>(sm.raw[r], j ? &wmap1 : &wmap0, k0, n, smem_u32(&sm.raw_full[r]));
-                ok = mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS);
-                if (!ok) {
-                    timed_out();
+                i8_tma_load<false>(sm.raw[r], at.j ? &wmap1 : &wmap0, k0, at.n * I8X_NC, smem_u32(&sm.raw_full[r]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == I8X_WARPS - 1) {
+        if (lane == 0 && !kI8WaitTest) {
+            I8DxPlace at(u0, C, NB, TM);
+            for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
+                const int m0 = at.tm * NT + (int)rank * (NT / 2);
+                const int s = armed % S;
+                if (sm.abort_flag || !mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
+                    if (!sm.abort_flag) timed_out();
                     break;
                 }
+                // the first CTA's barrier counts both CTAs' bytes
                 if (rank == 0) mbar_arrive_expect_tx(&sm.b_full[s], 2 * Cfg::B);
-                i8_tma_load<true>(sm.b[s], j ? &gmap1 : &gmap0, n, m0, cluster_addr(&sm.b_full[s], 0));
                 ++armed;
+                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, m0, cluster_addr(&sm.b_full[s], 0));
             }
-            if (!sm.abort_flag && !kI8WaitTest)
+            // the releases of the last stages arrive before the CTA ends
+            if (!sm.abort_flag)
                 for (int i = max(0, armed - S); i < armed; ++i)
                     if (!mbar_wait_bounded(&sm.empty[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS)) {
                         timed_out();
@@ -167,8 +198,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             constexpr uint32_t idesc = bf16_idesc(256, NT);
             int it = 0, seg = 0;
             bool ok = true;
-            for (int64_t u = u0; u < u1 && ok && !sm.abort_flag; ++seg) {
-                const int64_t end = min(u1, (u / C + 1) * C), first = u;
+            int64_t next = (u0 / C + 1) * C;
+            for (int64_t u = u0; u < u1 && ok && !sm.abort_flag; ++seg, next += C) {
+                const int64_t end = min(u1, next), first = u;
                 const int buf = seg & 1;
                 if (!mbar_wait_cluster(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u, I8_WAIT_NS)) {
                     timed_out();
@@ -194,11 +226,18 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 }
                 if (ok) i8_commit<true>(&sm.d_full[buf]);
             }
+            // the peer's last arrivals land before this CTA ends
+            if (ok && !sm.abort_flag)
+                for (int i = max(0, seg - 2); i < seg; ++i)
+                    if (!mbar_wait_cluster(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u, I8_WAIT_NS)) {
+                        timed_out();
+                        break;
+                    }
         }
         __syncwarp();
     } else if (warp < 6) {
         const int quad = warp & 3;
-        const uint32_t empty_bar[2] = {cluster_addr(&sm.d_empty[0], 0), cluster_addr(&sm.d_empty[1], 0)};
+        const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
         int seg = 0;
         for (int64_t u = u0; u < u1; ++seg) {
             const int64_t tile = u / C, t0 = tile * C, t1 = t0 + C;
@@ -282,7 +321,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             }
             i8_fence_before();
             __syncwarp();
-            if (lane == 0) cluster_arrive(empty_bar[buf]);
+            if (lane == 0) cluster_arrive(empty_bar + 8u * (uint32_t)buf);
             u = end;
         }
     } else {
@@ -293,11 +332,17 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         const int group = (warp - 6) / I8X_GWARPS, q = (warp - 6) % I8X_GWARPS, c = lane & 3;
         const int kg = ((lane >> 2) + 8 * c + 8 * q) & 31;
         const uint32_t row0 = (uint32_t)(4 * kg);
-        const int64_t n_units = u1 - u0;
-        for (int64_t it = group; it < n_units; it += I8X_GROUPS) {
-            const int r = (int)(it % R), s = (int)(it % S);
-            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.raw_full[r], (uint32_t)(it / R) & 1u, I8_WAIT_NS);
-            ok = ok && mbar_wait_bounded(&sm.empty[s], ((uint32_t)(it / S) & 1u) ^ 1u, I8_WAIT_NS);
+        const uint32_t n_units = (uint32_t)(u1 - u0);   // a CTA's run: far below 2^32
+        for (uint32_t it = group; it < n_units; it += I8X_GROUPS) {
+            const uint32_t r = it % R, s = it % S;
+            // The operand stage first: a parity wait can tell a phase only from
+            // its neighbour.  Units up to it - S are multiplied once empty[s]
+            // says so, so (R >= S) the copy of unit it - R has landed and
+            // raw_full[r] is at most one phase behind; asked the other way
+            // round, that copy (another group's unit) may still be in flight
+            // and the wait would pass a phase early.
+            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.empty[s], ((it / S) & 1u) ^ 1u, I8_WAIT_NS);
+            ok = ok && mbar_wait_bounded(&sm.raw_full[r], (it / R) & 1u, I8_WAIT_NS);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 if (lane == 0 && !sm.abort_flag) timed_out();
@@ -329,14 +374,12 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     }
     __syncthreads();
     if (sm.abort_flag) {
-        if (warp == 0 && lane == 0) {
-            // the last code copy may be one ahead of the last token copy
-            for (int i = max(0, armed + 1 - R); i < armed + 1; ++i)
-                mbar_wait_bounded(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u, I8_WAIT_NS / 64);
-            if (rank == 0)
-                for (int i = max(0, armed - S); i < armed; ++i)
-                    mbar_wait_bounded(&sm.b_full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
-        }
+        if (warp == 0 && lane == 0)
+            for (int i = max(0, armed - R); i < armed; ++i)
+                mbar_wait_bounded(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u, I8_WAIT_NS);
+        if (warp == I8X_WARPS - 1 && lane == 0 && rank == 0)
+            for (int i = max(0, armed - S); i < armed; ++i)
+                mbar_wait_bounded(&sm.b_full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
         if (warp == 1 && lane == 0 && rank == 0) {
             i8_commit<true>(&sm.drain);   // every MMA issued so far
             mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);

@@ -149,20 +149,25 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 
     if (warp == 0) {
         if (lane == 0) {
+            const int64_t tile = u0 / KB;
+            int kb = (int)(u0 - tile * KB), t = (int)(tile % T), mt = (int)(tile / T);
             for (int64_t u = u0; u < u1 && !sm.abort_flag; ++u, ++armed) {
                 const int s = armed % S;
                 if (!mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
                     timed_out();
                     break;
                 }
-                const int64_t tile = u / KB;
-                const int kc = (int)(u % KB) * I8_KC, t = (int)(tile % T), mt = (int)(tile / T);
+                const int kc = kb * I8_KC;
                 mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
                 if (kI8WaitTest) { ++armed; break; }   // armed, no copy
                 const uint32_t bar = smem_u32(&sm.full[s]);
                 i8_tma_load<false>(sm.st[s], &wmap0, kc, t * 128, bar);
                 if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, t * 128, bar);
                 i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, mt * NT, bar);
+                if (++kb == KB) {   // the next tile
+                    kb = 0;
+                    if (++t == T) { t = 0; ++mt; }
+                }
             }
         }
         __syncwarp();
@@ -170,8 +175,9 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         if (lane == 0) {
             constexpr uint32_t idesc = i8_idesc(128, NT);
             int it = 0;
-            for (int64_t u = u0; u < u1 && !sm.abort_flag;) {
-                const int64_t end = min(u1, (u / KB + 1) * KB);
+            int64_t next = (u0 / KB + 1) * KB;
+            for (int64_t u = u0; u < u1 && !sm.abort_flag; next += KB) {
+                const int64_t end = min(u1, next);
                 const int buf = segs % BUFS;
                 if (!mbar_wait_bounded(&sm.d_empty[buf], ((uint32_t)(segs / BUFS) & 1u) ^ 1u, I8_WAIT_NS)) {
                     timed_out();

@@ -153,13 +153,20 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 }
                 if (ok) i8_commit<true>(&sm.d_full[buf]);
             }
+            // the peer's last arrivals land before this CTA ends
+            if (ok && !sm.abort_flag)
+                for (int i = max(0, nt - 2); i < nt; ++i)
+                    if (!mbar_wait_cluster(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u, I8_WAIT_NS)) {
+                        timed_out();
+                        break;
+                    }
         }
         __syncwarp();
     } else {
         const int e = warp - 2, quad = warp & 3, half = e >> 2;
         float* pa = sm.piece[e][0];
         float* pb = sm.piece[e][Cfg::PIECES - 1];
-        const uint32_t empty_bar[2] = {cluster_addr(&sm.d_empty[0], 0), cluster_addr(&sm.d_empty[1], 0)};
+        const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
         int nt = 0;
         for (int64_t tile = pair; tile < tiles; tile += pairs, ++nt) {
             const int buf = nt & 1;
@@ -189,7 +196,7 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 if (c + 32 == BN / 2) {   // the accumulator is read: the next tile's MMAs may start
                     i8_fence_before();
                     __syncwarp();
-                    if (lane == 0) cluster_arrive(empty_bar[buf]);
+                    if (lane == 0) cluster_arrive(empty_bar + 8u * (uint32_t)buf);
                 }
                 __syncwarp();
                 const int64_t n = n0 + c + lane;

@@ -313,6 +313,26 @@ def test_linear_backward(mpq, M, N, K):
         assert guards_ok(buf, M, K)
 
 
+@pytest.mark.parametrize("M", [16, 64, 128, 512])
+def test_linear_backward_cold_weights(mpq, M):
+    """Long runs of code copies that come from HBM at their own pace (five
+    weight matrices in turn, none left in the cache), every result the same
+    bits as the first round's and that one within its tolerance."""
+    import torch
+    N, K = 2048, 14336
+    ws = [rand_i8(mpq, N, K, s, 1e-3) for s in range(5)]
+    dy = (torch.randn(M, N, generator=gen(7), device="cuda") * 0.1).to(torch.bfloat16)
+    first = [mpq.i8_linear_backward(w, dy) for w in ws]
+    for dx, w in zip(first, ws):
+        want, tol = dx64([(dy.double(), u * dy.double().abs(), hat(w))], N)
+        assert_dx(dx, want, tol)
+    space = torch.zeros(mpq.i8_linear_backward_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        again = [mpq.i8_linear_backward(w, dy, ws=space) for w in ws]
+        assert same(again, first)
+    mpq.check(space)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("M,F,K", [(1, 1, 1), (1, 96, 64), (3, 1371, 200), (16, 256, 512), (61, 1371, 1001),
                                    (64, 130, 129), (128, 512, 300), (129, 700, 640), (256, 300, 256), (300, 257, 1000),
