@@ -50,6 +50,26 @@ __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 #undef MPQ_I8_MMA
 }
 
+// One lane of the (converged) warp.  The MMA warp runs its loop as a whole and
+// only issues from this lane, so that stages, phases and descriptors stay
+// warp-uniform values: issued from a single-lane branch, each instruction's
+// operands were moved over one by one and a stage took some 870 cycles.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The four MMAs over 128 bytes of the contraction (32 bytes each) of operand
+// tiles at shared addresses a and b.
+template <bool PAIR, int KIND>
+__device__ __forceinline__ void i8_mma4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    const uint64_t da = i8_smem_desc(a), db = i8_smem_desc(b);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)   // 32 bytes = 2 units of the address field
+        i8_mma<PAIR, KIND>(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 || accumulate ? 1u : 0u);
+}
+
 // Arrive on `bar` (PAIR: on the barrier at the same address in both CTAs)
 // when the MMAs issued so far by this thread are done.
 template <bool PAIR>
@@ -131,24 +151,39 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// The waits on arrivals from the peer CTA.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-    const uint64_t t0 = global_timer_ns();
+// Waits for the phase of the given parity, for at most about I8_WAIT_NS;
+// false when that ran out.  The clock is read only after a while of polling:
+// reading it first cost the MMA thread some 300 cycles a stage.  CLUSTER:
+// arrivals may come from the peer CTA.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool i8_wait(uint64_t* bar, uint32_t parity) {
+    uint64_t t0 = 0;
     while (true) {
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < 16; ++i) {
             uint32_t ok;
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
-                : "memory");
+            if (CLUSTER)
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t"
+                    "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\t}"
+                    : "=r"(ok)
+                    : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+                    : "memory");
+            else
+                ok = mbar_try_wait_sleep(bar, parity, 100000u);
             if (ok) return true;
         }
-        if (global_timer_ns() - t0 > limit_ns) return false;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > I8_WAIT_NS) return false;
     }
+}
+
+// i8_wait by a whole warp: the same answer in every lane.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool i8_wait_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, i8_wait<CLUSTER>(bar, parity));
 }
 
 // Tensor-map copies global -> own shared memory.  PAIR: completes on a

@@ -52,7 +52,7 @@ struct I8DxSmem {
     uint8_t b[Cfg::S][(Cfg::B + 1023) / 1024 * 1024];
     uint8_t raw[Cfg::R][I8X_RAW];
     uint64_t raw_full[Cfg::R], raw_empty[Cfg::R];
-    uint64_t a_full[Cfg::S], b_full[Cfg::S], empty[Cfg::S];
+    uint64_t full[Cfg::S], empty[Cfg::S];   // full: both operands of the pair, in the first CTA
     uint64_t d_full[2], d_empty[2], drain;
     uint32_t tmem;
     volatile int abort_flag;
@@ -123,8 +123,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             mbar_init(&sm.raw_empty[s], I8X_GWARPS);
         }
         for (int s = 0; s < S; ++s) {
-            mbar_init(&sm.a_full[s], 2 * I8X_GWARPS);
-            mbar_init(&sm.b_full[s], 1);
+            mbar_init(&sm.full[s], 2 * I8X_GWARPS + 1);
             mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -158,7 +157,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
                 const int k0 = at.tk * 256 + (int)rank * 128;
                 const int r = armed % R;
-                if (sm.abort_flag || !mbar_wait_bounded(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u, I8_WAIT_NS)) {
+                if (sm.abort_flag || !i8_wait(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u)) {
                     if (!sm.abort_flag) timed_out();
                     break;
                 }
@@ -175,64 +174,57 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
                 const int m0 = at.tm * NT + (int)rank * (NT / 2);
                 const int s = armed % S;
-                if (sm.abort_flag || !mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
+                if (sm.abort_flag || !i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
                     if (!sm.abort_flag) timed_out();
                     break;
                 }
                 // the first CTA's barrier counts both CTAs' bytes
-                if (rank == 0) mbar_arrive_expect_tx(&sm.b_full[s], 2 * Cfg::B);
+                if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Cfg::B);
                 ++armed;
-                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, m0, cluster_addr(&sm.b_full[s], 0));
+                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, m0, cluster_addr(&sm.full[s], 0));
             }
             // the releases of the last stages arrive before the CTA ends
             if (!sm.abort_flag)
                 for (int i = max(0, armed - S); i < armed; ++i)
-                    if (!mbar_wait_bounded(&sm.empty[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS)) {
+                    if (!i8_wait(&sm.empty[i % S], (uint32_t)(i / S) & 1u)) {
                         timed_out();
                         break;
                     }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = bf16_idesc(256, NT);
-            int it = 0, seg = 0;
-            bool ok = true;
+            const bool issuer = elect_one();
+            int s = 0, seg = 0;
+            uint32_t ph = 0;
             int64_t next = (u0 / C + 1) * C;
-            for (int64_t u = u0; u < u1 && ok && !sm.abort_flag; ++seg, next += C) {
-                const int64_t end = min(u1, next), first = u;
+            bool ok = true;
+            for (int64_t u = u0; u < u1 && ok; next += C) {
+                const int n = (int)(min(u1, next) - u);
                 const int buf = seg & 1;
-                if (!mbar_wait_cluster(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u, I8_WAIT_NS)) {
-                    timed_out();
-                    break;
-                }
+                ok = i8_wait_warp<true>(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u);
+                if (!ok) break;
                 i8_fence_after();
-                for (; u < end; ++u, ++it) {
-                    const int s = it % S;
-                    const uint32_t ph = (uint32_t)(it / S) & 1u;
-                    if (!mbar_wait_cluster(&sm.a_full[s], ph, I8_WAIT_NS) ||
-                        !mbar_wait_bounded(&sm.b_full[s], ph, I8_WAIT_NS)) {
-                        timed_out();
-                        ok = false;
-                        break;
-                    }
+                for (int i = 0; i < n; ++i) {
+                    ok = i8_wait_warp<true>(&sm.full[s], ph);
+                    if (!ok) break;
                     i8_fence_after();
                     const uint32_t a = smem_u32(sm.a[s]), b = smem_u32(sm.b[s]);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        i8_mma<true, 1>(tmem + (uint32_t)(buf * NT), i8_smem_desc(a + kk * 32),
-                                        i8_smem_desc(b + kk * 32), idesc, u > first || kk > 0 ? 1u : 0u);
-                    i8_commit<true>(&sm.empty[s]);
+                    if (issuer) {
+                        i8_mma4<true, 1>(tmem + (uint32_t)(buf * NT), a, b, idesc, i > 0);
+                        i8_commit<true>(&sm.empty[s]);
+                        if (i == n - 1) i8_commit<true>(&sm.d_full[buf]);
+                    }
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                if (ok) i8_commit<true>(&sm.d_full[buf]);
+                if (ok) ++seg;
+                u += n;
             }
             // the peer's last arrivals land before this CTA ends
-            if (ok && !sm.abort_flag)
-                for (int i = max(0, seg - 2); i < seg; ++i)
-                    if (!mbar_wait_cluster(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u, I8_WAIT_NS)) {
-                        timed_out();
-                        break;
-                    }
+            for (int i = max(0, seg - 2); ok && i < seg; ++i)
+                ok = i8_wait_warp<true>(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u);
+            if (!ok && issuer) timed_out();
         }
         __syncwarp();
     } else if (warp < 6) {
@@ -243,7 +235,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             const int64_t tile = u / C, t0 = tile * C, t1 = t0 + C;
             const int64_t end = min(u1, t1);
             const int buf = seg & 1;
-            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u, I8_WAIT_NS);
+            bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
             if (!ok) {
                 if (lane == 0 && !sm.abort_flag) timed_out();
@@ -331,7 +323,12 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         // columns of group (g + 8 c + 8 q) % 32
         const int group = (warp - 6) / I8X_GWARPS, q = (warp - 6) % I8X_GWARPS, c = lane & 3;
         const int kg = ((lane >> 2) + 8 * c + 8 * q) & 31;
-        const uint32_t row0 = (uint32_t)(4 * kg);
+        uint32_t at[4];   // chunk of column 4 kg + j, block c (block c + 4: the other half of the row)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t row = (uint32_t)(4 * kg + j);
+            at[j] = (row >> 3) * 1024 + (row & 7) * 128 + (((uint32_t)c ^ (row & 7)) << 4);
+        }
         const uint32_t n_units = (uint32_t)(u1 - u0);   // a CTA's run: far below 2^32
         for (uint32_t it = group; it < n_units; it += I8X_GROUPS) {
             const uint32_t r = it % R, s = it % S;
@@ -341,8 +338,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             // raw_full[r] is at most one phase behind; asked the other way
             // round, that copy (another group's unit) may still be in flight
             // and the wait would pass a phase early.
-            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.empty[s], ((it / S) & 1u) ^ 1u, I8_WAIT_NS);
-            ok = ok && mbar_wait_bounded(&sm.raw_full[r], (it / R) & 1u, I8_WAIT_NS);
+            bool ok = !sm.abort_flag && i8_wait(&sm.empty[s], ((it / S) & 1u) ^ 1u);
+            ok = ok && i8_wait(&sm.raw_full[r], (it / R) & 1u);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 if (lane == 0 && !sm.abort_flag) timed_out();
@@ -358,17 +355,15 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t row = row0 + j;
                     const uint4 o = make_uint4(i8_pair_bf16(in[h][0], in[h][1], j), i8_pair_bf16(in[h][2], in[h][3], j),
                                                i8_pair_bf16(in[h][4], in[h][5], j), i8_pair_bf16(in[h][6], in[h][7], j));
-                    *reinterpret_cast<uint4*>(sm.a[s] + (row >> 3) * 1024 + (row & 7) * 128 +
-                                              (((4 * h + c) ^ (row & 7)) << 4)) = o;
+                    *reinterpret_cast<uint4*>(sm.a[s] + (at[j] ^ (uint32_t)(64 * h))) = o;
                 }
             fence_proxy_async_smem();   // to the tensor cores
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.raw_empty[r]);
-                cluster_arrive(cluster_addr(&sm.a_full[s], 0));
+                cluster_arrive(cluster_addr(&sm.full[s], 0));
             }
         }
     }
@@ -376,13 +371,10 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     if (sm.abort_flag) {
         if (warp == 0 && lane == 0)
             for (int i = max(0, armed - R); i < armed; ++i)
-                mbar_wait_bounded(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u, I8_WAIT_NS);
-        if (warp == I8X_WARPS - 1 && lane == 0 && rank == 0)
-            for (int i = max(0, armed - S); i < armed; ++i)
-                mbar_wait_bounded(&sm.b_full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
-        if (warp == 1 && lane == 0 && rank == 0) {
-            i8_commit<true>(&sm.drain);   // every MMA issued so far
-            mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);
+                i8_wait(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u);
+        if (warp == 1 && rank == 0) {   // every MMA issued so far
+            if (elect_one()) i8_commit<true>(&sm.drain);
+            i8_wait_warp(&sm.drain, 0u);
         }
         __syncwarp();
         i8_settle();

@@ -153,7 +153,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             int kb = (int)(u0 - tile * KB), t = (int)(tile % T), mt = (int)(tile / T);
             for (int64_t u = u0; u < u1 && !sm.abort_flag; ++u, ++armed) {
                 const int s = armed % S;
-                if (!mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
+                if (!i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
                     timed_out();
                     break;
                 }
@@ -172,44 +172,37 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = i8_idesc(128, NT);
-            int it = 0;
-            int64_t next = (u0 / KB + 1) * KB;
-            for (int64_t u = u0; u < u1 && !sm.abort_flag; next += KB) {
-                const int64_t end = min(u1, next);
-                const int buf = segs % BUFS;
-                if (!mbar_wait_bounded(&sm.d_empty[buf], ((uint32_t)(segs / BUFS) & 1u) ^ 1u, I8_WAIT_NS)) {
-                    timed_out();
-                    break;
-                }
+        constexpr uint32_t idesc = i8_idesc(128, NT);
+        const bool issuer = elect_one();
+        int s = 0;
+        uint32_t ph = 0;
+        int64_t next = (u0 / KB + 1) * KB;
+        bool ok = true;
+        for (int64_t u = u0; u < u1 && ok; next += KB) {
+            const int n = (int)(min(u1, next) - u);
+            const int buf = segs % BUFS;
+            ok = i8_wait_warp(&sm.d_empty[buf], ((uint32_t)(segs / BUFS) & 1u) ^ 1u);
+            if (!ok) break;
+            i8_fence_after();
+            for (int i = 0; i < n; ++i) {
+                ok = i8_wait_warp(&sm.full[s], ph);
+                if (!ok) break;
                 i8_fence_after();
-                const int64_t first = u;
-                bool ok = true;
-                for (; u < end; ++u, ++it) {
-                    const int s = it % S;
-                    if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(it / S) & 1u, I8_WAIT_NS)) {
-                        timed_out();
-                        ok = false;
-                        break;
-                    }
-                    i8_fence_after();
-                    const uint32_t st = smem_u32(sm.st[s]);
+                const uint32_t st = smem_u32(sm.st[s]);
+                if (issuer) {
 #pragma unroll
                     for (int j = 0; j < NW; ++j)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            i8_mma<false, 0>(tmem + (uint32_t)((buf * NW + j) * NT),
-                                             i8_smem_desc(st + j * Cfg::W_BYTES + kk * 32),
-                                             i8_smem_desc(st + NW * Cfg::W_BYTES + kk * 32), idesc,
-                                             u > first || kk > 0 ? 1u : 0u);
+                        i8_mma4<false, 0>(tmem + (uint32_t)((buf * NW + j) * NT), st + j * Cfg::W_BYTES,
+                                          st + NW * Cfg::W_BYTES, idesc, i > 0);
                     i8_commit<false>(&sm.empty[s]);
+                    if (i == n - 1) i8_commit<false>(&sm.d_full[buf]);
                 }
-                if (!ok) break;
-                i8_commit<false>(&sm.d_full[buf]);
-                ++segs;
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
+            if (ok) ++segs;
+            u += n;
         }
+        if (!ok && issuer) timed_out();
         __syncwarp();
     } else {
         const int quad = warp & 3;
@@ -218,7 +211,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             const int64_t tile = u / KB, t0 = tile * KB, t1 = t0 + KB;
             const int64_t end = min(u1, t1);
             const int buf = seg % BUFS;
-            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.d_full[buf], (uint32_t)(seg / BUFS) & 1u, I8_WAIT_NS);
+            bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg / BUFS) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
             if (!ok) {
                 if (lane == 0 && !sm.abort_flag) timed_out();
@@ -313,13 +306,13 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     // copies and MMAs in flight land before shared memory and TMEM are given
     // up (after an abort they may be; else this is already so)
     __syncthreads();
-    if (sm.abort_flag && lane == 0) {
-        if (warp == 0)
+    if (sm.abort_flag) {
+        if (warp == 0 && lane == 0)
             for (int i = max(0, armed - S); i < armed; ++i)
-                mbar_wait_bounded(&sm.full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
-        if (warp == 1) {
-            i8_commit<false>(&sm.drain);   // every MMA issued so far
-            mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);
+                i8_wait(&sm.full[i % S], (uint32_t)(i / S) & 1u);
+        if (warp == 1) {   // every MMA issued so far
+            if (elect_one()) i8_commit<false>(&sm.drain);
+            i8_wait_warp(&sm.drain, 0u);
         }
     }
     i8_fence_before();

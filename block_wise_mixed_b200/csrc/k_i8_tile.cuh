@@ -101,7 +101,7 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 const CUtensorMap* wmap = NW == 2 && rank == 1 ? &wmap1 : &wmap0;
                 for (int kb = 0; kb < KB; ++kb) {
                     const int s = armed % S;
-                    if (sm.abort_flag || !mbar_wait_bounded(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u, I8_WAIT_NS)) {
+                    if (sm.abort_flag || !i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
                         if (!sm.abort_flag) timed_out();
                         stop = true;
                         break;
@@ -118,48 +118,42 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             // the releases of the last stages arrive before the CTA ends
             if (!sm.abort_flag && !kI8WaitTest)
                 for (int i = max(0, armed - S); i < armed; ++i)
-                    if (!mbar_wait_bounded(&sm.empty[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS)) {
+                    if (!i8_wait(&sm.empty[i % S], (uint32_t)(i / S) & 1u)) {
                         timed_out();
                         break;
                     }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = i8_idesc(256, 256);
-            int it = 0, nt = 0;
+            const bool issuer = elect_one();
+            int s = 0, nt = 0;
+            uint32_t ph = 0;
             bool ok = true;
-            for (int64_t tile = pair; tile < tiles && ok && !sm.abort_flag; tile += pairs, ++nt) {
+            for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
                 const int buf = nt & 1;
-                if (!mbar_wait_cluster(&sm.d_empty[buf], ((uint32_t)(nt >> 1) & 1u) ^ 1u, I8_WAIT_NS)) {
-                    timed_out();
-                    break;
-                }
+                ok = i8_wait_warp<true>(&sm.d_empty[buf], ((uint32_t)(nt >> 1) & 1u) ^ 1u);
+                if (!ok) break;
                 i8_fence_after();
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % S;
-                    if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(it / S) & 1u, I8_WAIT_NS)) {
-                        timed_out();
-                        ok = false;
-                        break;
-                    }
+                for (int kb = 0; kb < KB; ++kb) {
+                    ok = i8_wait_warp(&sm.full[s], ph);
+                    if (!ok) break;
                     i8_fence_after();
                     const uint32_t st = smem_u32(sm.st[s]);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        i8_mma<true, 0>(tmem + (uint32_t)(buf * 256), i8_smem_desc(st + kk * 32),
-                                        i8_smem_desc(st + 128 * I8_KC + kk * 32), idesc, kb > 0 || kk > 0 ? 1u : 0u);
-                    i8_commit<true>(&sm.empty[s]);
+                    if (issuer) {
+                        i8_mma4<true, 0>(tmem + (uint32_t)(buf * 256), st, st + 128 * I8_KC, idesc, kb > 0);
+                        i8_commit<true>(&sm.empty[s]);
+                        if (kb == KB - 1) i8_commit<true>(&sm.d_full[buf]);
+                    }
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                if (ok) i8_commit<true>(&sm.d_full[buf]);
+                if (ok) ++nt;
             }
             // the peer's last arrivals land before this CTA ends
-            if (ok && !sm.abort_flag)
-                for (int i = max(0, nt - 2); i < nt; ++i)
-                    if (!mbar_wait_cluster(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u, I8_WAIT_NS)) {
-                        timed_out();
-                        break;
-                    }
+            for (int i = max(0, nt - 2); ok && i < nt; ++i)
+                ok = i8_wait_warp<true>(&sm.d_empty[i & 1], (uint32_t)(i >> 1) & 1u);
+            if (!ok && issuer) timed_out();
         }
         __syncwarp();
     } else {
@@ -174,7 +168,7 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
             const int64_t n0 = (tile / TM) * BN + half * (BN / 2);
             const int rows = (int)max((int64_t)0, min((int64_t)32, p.M - m0));
             const float xs = lane < rows ? p.xs[m0 + lane] : 0.f;
-            bool ok = !sm.abort_flag && mbar_wait_bounded(&sm.d_full[buf], (uint32_t)(nt >> 1) & 1u, I8_WAIT_NS);
+            bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(nt >> 1) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
             if (!ok) {
                 if (lane == 0 && !sm.abort_flag) timed_out();
@@ -221,10 +215,10 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     if (sm.abort_flag) {
         if (warp == 0 && lane == 0 && rank == 0)
             for (int i = max(0, armed - S); i < armed; ++i)
-                mbar_wait_bounded(&sm.full[i % S], (uint32_t)(i / S) & 1u, I8_WAIT_NS);
-        if (warp == 1 && lane == 0 && rank == 0) {
-            i8_commit<true>(&sm.drain);   // every MMA issued so far
-            mbar_wait_bounded(&sm.drain, 0u, I8_WAIT_NS);
+                i8_wait(&sm.full[i % S], (uint32_t)(i / S) & 1u);
+        if (warp == 1 && rank == 0) {   // every MMA issued so far
+            if (elect_one()) i8_commit<true>(&sm.drain);
+            i8_wait_warp(&sm.drain, 0u);
         }
         __syncwarp();
         i8_settle();
