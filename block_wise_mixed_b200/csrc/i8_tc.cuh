@@ -207,6 +207,12 @@ __device__ __forceinline__ void i8_tma_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+__device__ __forceinline__ uint32_t i8_load_acquire(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // After an abort: gives copies and arrivals in flight, which no barrier of
 // this CTA tracks any more, time to land before the memory is given up.
 __device__ __forceinline__ void i8_settle() {

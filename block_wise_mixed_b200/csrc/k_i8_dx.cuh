@@ -40,8 +40,10 @@ constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
 template <int NT>
 struct I8DxCfg {
     static constexpr int B = NT / 2 * I8X_NC * 2;              // this CTA's tokens
-    static constexpr int S = NT == 256 ? 5 : NT == 128 ? 6 : 8;        // operand stages
-    static constexpr int R = NT == 256 ? 6 : 8;                        // code stages
+    // Operand stages, and code stages with what shared memory is left: few
+    // tokens wait for the codes, many for the operands.
+    static constexpr int S = 5;
+    static constexpr int R = NT == 256 ? 6 : NT == 128 ? 10 : NT == 64 ? 12 : 14;
     static constexpr uint32_t COLS = 2 * NT;                   // double-buffered accumulator
 };
 
@@ -249,64 +251,65 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             auto slot_of = [&](int64_t c) {
                 return p.slots + (((c * 2 + (c == c0 ? 1 : 0)) * 2 + rank) * NT) * 128 + quad * 32 + lane;
             };
+            // A cut tile: when all others have arrived already (the usual case
+            // for the run that holds the tile's start, its last work), this
+            // one only adds; else it leaves its part and counts itself in.
+            uint32_t* counter = p.counters + (c0 * 2 + rank) * 4 + quad;
+            const uint32_t others = (uint32_t)(c1 - c0);
             bool mine = true;
             if (c0 != c1) {
-                float* slot = slot_of(pair);
-                for (int c = 0; c < mc; c += 16) {
-                    uint32_t r[16];
-                    i8_tmem_ld16(taddr + (uint32_t)c, r);
-                    i8_tmem_wait();
+                uint32_t seen = 0;
+                if (lane == 0) seen = i8_load_acquire(counter);
+                if (__shfl_sync(0xffffffffu, seen, 0) != others) {
+                    float* slot = slot_of(pair);
+                    for (int c = 0; c < mc; c += 32) {
+                        uint32_t r[32];
+                        i8_tmem_ld32(taddr + (uint32_t)c, r);
+                        i8_tmem_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < mc) slot[(c + i) * 128] = __uint_as_float(r[i]);
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < mc) slot[(c + i) * 128] = __uint_as_float(r[i]);
+                    }
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) seen = atomic_add_acq_rel_gpu(counter, 1u);
+                    mine = __shfl_sync(0xffffffffu, seen, 0) == others;
                 }
-                __threadfence();
-                __syncwarp();
-                uint32_t* counter = p.counters + (c0 * 2 + rank) * 4 + quad;
-                uint32_t old = 0;
-                if (lane == 0) old = atomic_add_acq_rel_gpu(counter, 1u);
-                old = __shfl_sync(0xffffffffu, old, 0);
-                mine = old == (uint32_t)(c1 - c0);
                 if (mine) {
-                    if (lane == 0) *counter = 0u;
+                    if (lane == 0) *counter = 0u;   // clean for the next call
                     __threadfence();
                 }
             }
             if (mine) {
-                for (int c = 0; c < mc; c += 8) {
-                    float v[8];
-                    if (c0 == c1) {
-                        uint32_t r[8];
-                        i8_tmem_ld8(taddr + (uint32_t)c, r);
-                        i8_tmem_wait();
+                for (int c = 0; c < mc; c += 32) {
+                    float v[32];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-                    } else {
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int64_t o = c0; o <= c1; ++o) {   // in the order of the runs
+                        uint32_t t[32];
+                        if (o == pair) {
+                            i8_tmem_ld32(taddr + (uint32_t)c, t);
+                            i8_tmem_wait();
+                        } else {
+                            const float* slot = slot_of(o);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                        // in the order of the runs; four contributors' loads
-                        // in flight at a time
-                        for (int64_t o = c0; o <= c1; o += 4) {
-                            float t[4][8];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (o + q <= c1) {
-                                    const float* slot = slot_of(o + q);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        if (c + i < mc) t[q][i] = __ldcg(slot + (c + i) * 128);
-                                }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (o + q <= c1)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) v[i] += t[q][i];
+                            for (int i = 0; i < 32; ++i)
+                                t[i] = c + i < mc ? __float_as_uint(__ldcg(slot + (c + i) * 128)) : 0u;
                         }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(t[i]);
                     }
                     if (k < p.K) {
+                        uint16_t* dx = p.dx + (m0 + c) * p.lddx + k;
+                        const int left = mc - c;
+                        if (left >= 32) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c + i < mc) p.dx[(m0 + c + i) * p.lddx + k] = (uint16_t)pack_bf16(v[i], 0.f);
+                            for (int i = 0; i < 32; ++i, dx += p.lddx) *dx = (uint16_t)pack_bf16(v[i], 0.f);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i, dx += p.lddx)
+                                if (i < left) *dx = (uint16_t)pack_bf16(v[i], 0.f);
+                        }
                     }
                     __syncwarp();
                 }

@@ -65,33 +65,67 @@ struct I8Product {
     int32_t* slots;      // partial sums
 };
 
-// What an output element becomes of its sums.  MODE 0: linear, 1: gated,
-// 2: the gradients of gate and up.
+// A column of outputs: channel n of tokens m, m + 1, ..., with the addresses
+// counted along (64-bit products for every element cost more than its
+// arithmetic).  MODE 0: linear, 1: gated, 2: the gradients of gate and up.
 template <int MODE, int ACT>
-__device__ __forceinline__ void i8_finish(const I8Product& p, int64_t m, int64_t n, int acc0, int acc1, float ws0,
-                                          float ws1, float xs, float dh) {
-    const float a = ((float)acc0 * ws0) * xs;
-    if (MODE == 0) {
-        if (p.y_bf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_bf16(a, 0.f);
-        else static_cast<float*>(p.y)[m * p.ldy + n] = a;
-        return;
+struct I8Column {
+    uint8_t* y;
+    const uint16_t* dh;
+    uint16_t *d0, *d1, *g;
+    int64_t ystep, dhstep, dstep, gstep, up_off;
+    float ws0, ws1;
+    bool bf16;
+
+    __device__ __forceinline__ I8Column(const I8Product& p, int64_t m, int64_t n, float ws0_, float ws1_)
+        : ws0(ws0_), ws1(ws1_) {
+        if (MODE < 2) {
+            bf16 = p.y_bf16 != 0;
+            ystep = p.ldy * (bf16 ? 2 : 4);
+            y = static_cast<uint8_t*>(p.y) + m * ystep + n * (bf16 ? 2 : 4);
+        } else {
+            dhstep = p.lddh;
+            dh = p.dh + m * dhstep + n;
+            dstep = p.ldd;
+            d0 = p.d[0] ? p.d[0] + m * dstep + n : nullptr;
+            d1 = p.d[0] ? p.d[1] + m * dstep + n : nullptr;
+            gstep = p.ldg;
+            g = p.g + m * gstep + n;
+            up_off = p.up_off;
+        }
     }
-    const float b = ((float)acc1 * ws1) * xs;
-    const Gate g = gate_eval<ACT>(a);
-    if (MODE == 1) {
-        const float h = g.act * b;
-        if (p.y_bf16) static_cast<uint16_t*>(p.y)[m * p.ldy + n] = (uint16_t)pack_bf16(h, 0.f);
-        else static_cast<float*>(p.y)[m * p.ldy + n] = h;
-        return;
+    __device__ __forceinline__ float load_dh() const { return MODE == 2 ? I8Elem<true>::get(*dh) : 0.f; }
+    __device__ __forceinline__ void next_dh() { if (MODE == 2) dh += dhstep; }
+    __device__ __forceinline__ void next() {
+        if (MODE < 2) {
+            y += ystep;
+        } else {
+            if (d0) { d0 += dstep; d1 += dstep; }
+            g += gstep;
+        }
     }
-    const float dg = dh * b * g.grad, du = dh * g.act;
-    if (p.d[0]) {
-        p.d[0][m * p.ldd + n] = (uint16_t)pack_bf16(dg, 0.f);
-        p.d[1][m * p.ldd + n] = (uint16_t)pack_bf16(du, 0.f);
+    __device__ __forceinline__ void put(int acc0, int acc1, float xs, float dhv) const {
+        const float a = ((float)acc0 * ws0) * xs;
+        float v = a;
+        if (MODE > 0) {
+            const float b = ((float)acc1 * ws1) * xs;
+            const Gate gt = gate_eval<ACT>(a);
+            if (MODE == 2) {
+                const float dg = dhv * b * gt.grad, du = dhv * gt.act;
+                if (d0) {
+                    *d0 = (uint16_t)pack_bf16(dg, 0.f);
+                    *d1 = (uint16_t)pack_bf16(du, 0.f);
+                }
+                g[0] = (uint16_t)pack_bf16(dg * ws0, 0.f);
+                g[up_off] = (uint16_t)pack_bf16(du * ws1, 0.f);
+                return;
+            }
+            v = gt.act * b;
+        }
+        if (bf16) *reinterpret_cast<uint16_t*>(y) = (uint16_t)pack_bf16(v, 0.f);
+        else *reinterpret_cast<float*>(y) = v;
     }
-    p.g[m * p.ldg + n] = (uint16_t)pack_bf16(dg * ws0, 0.f);
-    p.g[m * p.ldg + p.up_off + n] = (uint16_t)pack_bf16(du * ws1, 0.f);
-}
+};
 
 // Unit u belongs to CTA u * G / units (rounded down the same way as the
 // runs' ends): run c is [c * units / G, (c + 1) * units / G).
@@ -229,43 +263,45 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             auto slot_of = [&](int64_t c) {
                 return p.slots + ((c * 2 + (c == c0 ? 1 : 0)) * NW * NT) * 128 + quad * 32 + lane;
             };
+            // A cut tile: when all others have arrived already, this one only
+            // adds; else it leaves its part and counts itself in.
+            uint32_t* counter = p.counters + c0 * 4 + quad;
+            const uint32_t others = (uint32_t)(c1 - c0);
             bool mine = true;   // this warp writes the results
             if (c0 != c1) {
-                int32_t* slot = slot_of(cta);
-                for (int c = 0; c < mc; c += 16) {
+                uint32_t seen = 0;
+                if (lane == 0) seen = i8_load_acquire(counter);
+                if (__shfl_sync(0xffffffffu, seen, 0) != others) {
+                    int32_t* slot = slot_of(cta);
+                    for (int c = 0; c < mc; c += 16) {
 #pragma unroll
-                    for (int j = 0; j < NW; ++j) {
-                        uint32_t r[16];
-                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
-                        i8_tmem_wait();
+                        for (int j = 0; j < NW; ++j) {
+                            uint32_t r[16];
+                            i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
+                            i8_tmem_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[i];
+                            for (int i = 0; i < 16; ++i)
+                                if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[i];
+                        }
                     }
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) seen = atomic_add_acq_rel_gpu(counter, 1u);
+                    mine = __shfl_sync(0xffffffffu, seen, 0) == others;
                 }
-                __threadfence();
-                __syncwarp();
-                uint32_t old = 0;
-                if (lane == 0) old = atomic_add_acq_rel_gpu(&p.counters[c0 * 4 + quad], 1u);
-                old = __shfl_sync(0xffffffffu, old, 0);
-                mine = old == (uint32_t)(c1 - c0);
                 if (mine) {
-                    if (lane == 0) p.counters[c0 * 4 + quad] = 0u;   // clean for the next call
+                    if (lane == 0) *counter = 0u;   // clean for the next call
                     __threadfence();
                 }
             }
             if (mine) {
                 for (int c = 0; c < mc; c += 16) {
                     int acc[NW][16];
+                    if (c0 != c1) {
 #pragma unroll
-                    for (int j = 0; j < NW; ++j) {
-                        uint32_t r[16];
-                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
-                        i8_tmem_wait();
+                        for (int j = 0; j < NW; ++j)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[j][i] = (int)r[i];
-                    }
-                    if (c0 != c1)
+                            for (int i = 0; i < 16; ++i) acc[j][i] = 0;
                         for (int64_t o = c0; o <= c1; o += 2) {   // two contributors' loads in flight
                             int t[2][NW][16];
 #pragma unroll
@@ -285,13 +321,29 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) acc[j][i] += t[q][j][i];
                         }
+                    }
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint32_t r[16];
+                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
+                        i8_tmem_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[j][i] = (c0 != c1 ? acc[j][i] : 0) + (int)r[i];
+                    }
                     if (in) {
+                        I8Column<MODE, ACT> col(p, m0 + c, n, ws0, ws1);
+                        const float* xs = p.xs + m0 + c;
+                        const int left = mc - c;
+                        float dh[MODE == 2 ? 16 : 1];
+                        if (MODE == 2)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i < left) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (c + i < mc) {
-                                const int64_t m = m0 + c + i;
-                                const float dh = MODE == 2 ? I8Elem<true>::get(p.dh[m * p.lddh + n]) : 0.f;
-                                i8_finish<MODE, ACT>(p, m, n, acc[0][i], acc[NW - 1][i], ws0, ws1, p.xs[m], dh);
+                            if (i < left) {
+                                col.put(acc[0][i], acc[NW - 1][i], xs[i], dh[MODE == 2 ? i : 0]);
+                                col.next();
                             }
                     }
                     __syncwarp();

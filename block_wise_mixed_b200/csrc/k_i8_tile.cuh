@@ -196,15 +196,23 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 const int64_t n = n0 + c + lane;
                 const bool in = n < p.N;
                 const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
-#pragma unroll 8
-                for (int i = 0; i < rows; ++i) {
-                    const int a0 = __float_as_int(pa[i * 32 + (lane ^ i)]);
-                    const int a1 = NW == 2 ? __float_as_int(pb[i * 32 + (lane ^ i)]) : 0;
-                    const float s = __shfl_sync(0xffffffffu, xs, i);
-                    const int64_t m = m0 + i;
-                    if (in) {
-                        const float dh = MODE == 2 ? I8Elem<true>::get(p.dh[m * p.lddh + n]) : 0.f;
-                        i8_finish<MODE, ACT>(p, m, n, a0, a1, ws0, ws1, s, dh);
+                I8Column<MODE, ACT> col(p, m0, n, ws0, ws1);
+                for (int i0 = 0; i0 < rows; i0 += 8) {
+                    float dh[MODE == 2 ? 8 : 1];
+                    if (MODE == 2)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (in && i0 + i < rows) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i0 + i;
+                        const int a0 = __float_as_int(pa[r * 32 + (lane ^ r)]);
+                        const int a1 = NW == 2 ? __float_as_int(pb[r * 32 + (lane ^ r)]) : 0;
+                        const float s = __shfl_sync(0xffffffffu, xs, r);
+                        if (in && r < rows) {
+                            col.put(a0, a1, s, dh[MODE == 2 ? i : 0]);
+                            col.next();
+                        }
                     }
                 }
                 __syncwarp();
