@@ -8,7 +8,7 @@
 // tokens over the two SMs of a cluster.
 //
 // The codes lie with k along the rows and the contraction across them; the
-// operand wants the contraction along its rows, in bf16.  Sixteen warps turn
+// operand wants the contraction along its rows, in bf16.  Twelve warps turn
 // each 64 x 128 code tile (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
 // one byte permute, and makes them bf16 with two masks and one subtraction:
@@ -30,7 +30,7 @@
 
 namespace mpq {
 
-constexpr int I8X_GROUPS = 4;               // converter groups, a stage each in turn
+constexpr int I8X_GROUPS = 3;               // converter groups, a stage each in turn
 constexpr int I8X_GWARPS = 4;               // warps of a group
 constexpr int I8X_WARPS = 7 + I8X_GROUPS * I8X_GWARPS;
 constexpr int I8X_NC = 64;                  // channels in a stage
@@ -154,45 +154,48 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     int armed = 0;   // units whose copies were issued (warp 0: codes, the last warp: tokens)
 
     if (warp == 0) {
-        if (lane == 0) {
-            I8DxPlace at(u0, C, NB, TM);
-            for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
-                const int k0 = at.tk * 256 + (int)rank * 128;
-                const int r = armed % R;
-                if (sm.abort_flag || !i8_wait(&sm.raw_empty[r], ((uint32_t)(armed / R) & 1u) ^ 1u)) {
-                    if (!sm.abort_flag) timed_out();
-                    break;
-                }
+        const bool issuer = elect_one();
+        I8DxPlace at(u0, C, NB, TM);
+        int r = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
+            ok = i8_wait_warp(&sm.raw_empty[r], ph);
+            if (!ok) break;
+            ++armed;
+            if (issuer) {
                 mbar_arrive_expect_tx(&sm.raw_full[r], I8X_RAW);
-                ++armed;
-                if (kI8WaitTest) break;   // armed, no copy
-                i8_tma_load<false>(sm.raw[r], at.j ? &wmap1 : &wmap0, k0, at.n * I8X_NC, smem_u32(&sm.raw_full[r]));
+                if (!kI8WaitTest)
+                    i8_tma_load<false>(sm.raw[r], at.j ? &wmap1 : &wmap0, at.tk * 256 + (int)rank * 128, at.n * I8X_NC,
+                                       smem_u32(&sm.raw_full[r]));
             }
+            if (kI8WaitTest) break;   // armed, no copy
+            if (++r == R) { r = 0; ph ^= 1u; }
         }
+        if (!ok && issuer) timed_out();
         __syncwarp();
     } else if (warp == I8X_WARPS - 1) {
-        if (lane == 0 && !kI8WaitTest) {
-            I8DxPlace at(u0, C, NB, TM);
-            for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
-                const int m0 = at.tm * NT + (int)rank * (NT / 2);
-                const int s = armed % S;
-                if (sm.abort_flag || !i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
-                    if (!sm.abort_flag) timed_out();
-                    break;
-                }
+        const bool issuer = elect_one();
+        I8DxPlace at(u0, C, NB, TM);
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = !kI8WaitTest;
+        for (int64_t u = u0; u < u1 && ok; ++u, at.next(C, NB, TM)) {
+            ok = i8_wait_warp(&sm.empty[s], ph);
+            if (!ok) break;
+            ++armed;
+            if (issuer) {
                 // the first CTA's barrier counts both CTAs' bytes
                 if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Cfg::B);
-                ++armed;
-                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, m0, cluster_addr(&sm.full[s], 0));
+                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, at.tm * NT + (int)rank * (NT / 2),
+                                  cluster_addr(&sm.full[s], 0));
             }
-            // the releases of the last stages arrive before the CTA ends
-            if (!sm.abort_flag)
-                for (int i = max(0, armed - S); i < armed; ++i)
-                    if (!i8_wait(&sm.empty[i % S], (uint32_t)(i / S) & 1u)) {
-                        timed_out();
-                        break;
-                    }
+            if (++s == S) { s = 0; ph ^= 1u; }
         }
+        // the releases of the last stages arrive before the CTA ends
+        for (int i = max(0, armed - S); ok && i < armed; ++i)
+            ok = i8_wait_warp(&sm.empty[i % S], (uint32_t)(i / S) & 1u);
+        if (!ok && issuer && !kI8WaitTest) timed_out();
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -320,7 +323,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             u = end;
         }
     } else {
-        // converters: a group takes every fourth stage, so that four stages'
+        // converters: a group takes every third stage, so that three stages'
         // waits, loads and fences overlap.  Warp q of it takes rows 0 .. 31,
         // then 32 .. 63; lane (c, g) the eight rows of block c and the four
         // columns of group (g + 8 c + 8 q) % 32
@@ -372,9 +375,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     }
     __syncthreads();
     if (sm.abort_flag) {
-        if (warp == 0 && lane == 0)
+        if (warp == 0)
             for (int i = max(0, armed - R); i < armed; ++i)
-                i8_wait(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u);
+                i8_wait_warp(&sm.raw_full[i % R], (uint32_t)(i / R) & 1u);
         if (warp == 1 && rank == 0) {   // every MMA issued so far
             if (elect_one()) i8_commit<true>(&sm.drain);
             i8_wait_warp(&sm.drain, 0u);

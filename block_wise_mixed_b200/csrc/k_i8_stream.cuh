@@ -182,28 +182,33 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     int armed = 0, segs = 0;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const int64_t tile = u0 / KB;
-            int kb = (int)(u0 - tile * KB), t = (int)(tile % T), mt = (int)(tile / T);
-            for (int64_t u = u0; u < u1 && !sm.abort_flag; ++u, ++armed) {
-                const int s = armed % S;
-                if (!i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
-                    timed_out();
-                    break;
-                }
-                const int kc = kb * I8_KC;
+        const bool issuer = elect_one();
+        const int64_t tile = u0 / KB;
+        int kb = (int)(u0 - tile * KB), t = (int)(tile % T), mt = (int)(tile / T), s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int64_t u = u0; u < u1; ++u) {
+            ok = i8_wait_warp(&sm.empty[s], ph);
+            if (!ok) break;
+            ++armed;
+            if (issuer) {
                 mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
-                if (kI8WaitTest) { ++armed; break; }   // armed, no copy
-                const uint32_t bar = smem_u32(&sm.full[s]);
-                i8_tma_load<false>(sm.st[s], &wmap0, kc, t * 128, bar);
-                if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, t * 128, bar);
-                i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, mt * NT, bar);
-                if (++kb == KB) {   // the next tile
-                    kb = 0;
-                    if (++t == T) { t = 0; ++mt; }
+                if (!kI8WaitTest) {
+                    const uint32_t bar = smem_u32(&sm.full[s]);
+                    const int kc = kb * I8_KC;
+                    i8_tma_load<false>(sm.st[s], &wmap0, kc, t * 128, bar);
+                    if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, t * 128, bar);
+                    i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, mt * NT, bar);
                 }
             }
+            if (kI8WaitTest) break;   // armed, no copy
+            if (++s == S) { s = 0; ph ^= 1u; }
+            if (++kb == KB) {   // the next tile
+                kb = 0;
+                if (++t == T) { t = 0; ++mt; }
+            }
         }
+        if (!ok && issuer) timed_out();
         __syncwarp();
     } else if (warp == 1) {
         constexpr uint32_t idesc = i8_idesc(128, NT);
@@ -359,9 +364,9 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     // up (after an abort they may be; else this is already so)
     __syncthreads();
     if (sm.abort_flag) {
-        if (warp == 0 && lane == 0)
+        if (warp == 0)
             for (int i = max(0, armed - S); i < armed; ++i)
-                i8_wait(&sm.full[i % S], (uint32_t)(i / S) & 1u);
+                i8_wait_warp(&sm.full[i % S], (uint32_t)(i / S) & 1u);
         if (warp == 1) {   // every MMA issued so far
             if (elect_one()) i8_commit<false>(&sm.drain);
             i8_wait_warp(&sm.drain, 0u);

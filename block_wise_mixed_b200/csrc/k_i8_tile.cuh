@@ -93,36 +93,36 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     int armed = 0;
 
     if (warp == 0) {
-        if (lane == 0) {
-            bool stop = false;
-            for (int64_t tile = pair; tile < tiles && !stop; tile += pairs) {
-                const int m0 = (int)(tile % TM) * 256 + (int)rank * 128;
-                const int n0 = (int)(tile / TM) * BN + (NW == 1 ? (int)rank * 128 : 0);
-                const CUtensorMap* wmap = NW == 2 && rank == 1 ? &wmap1 : &wmap0;
-                for (int kb = 0; kb < KB; ++kb) {
-                    const int s = armed % S;
-                    if (sm.abort_flag || !i8_wait(&sm.empty[s], ((uint32_t)(armed / S) & 1u) ^ 1u)) {
-                        if (!sm.abort_flag) timed_out();
-                        stop = true;
-                        break;
-                    }
+        const bool issuer = elect_one();
+        int s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int64_t tile = pair; tile < tiles && ok; tile += pairs) {
+            const int m0 = (int)(tile % TM) * 256 + (int)rank * 128;
+            const int n0 = (int)(tile / TM) * BN + (NW == 1 ? (int)rank * 128 : 0);
+            const CUtensorMap* wmap = NW == 2 && rank == 1 ? &wmap1 : &wmap0;
+            for (int kb = 0; kb < KB; ++kb) {
+                ok = i8_wait_warp(&sm.empty[s], ph);
+                if (!ok) break;
+                ++armed;
+                if (issuer) {
                     // the first CTA's barrier counts both CTAs' bytes
                     if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Cfg::STAGE);
-                    ++armed;
-                    if (kI8WaitTest) { stop = true; break; }   // armed, no copy
-                    const uint32_t bar = cluster_addr(&sm.full[s], 0);
-                    i8_tma_load<true>(sm.st[s], &xmap, kb * I8_KC, m0, bar);
-                    i8_tma_load<true>(sm.st[s] + 128 * I8_KC, wmap, kb * I8_KC, n0, bar);
-                }
-            }
-            // the releases of the last stages arrive before the CTA ends
-            if (!sm.abort_flag && !kI8WaitTest)
-                for (int i = max(0, armed - S); i < armed; ++i)
-                    if (!i8_wait(&sm.empty[i % S], (uint32_t)(i / S) & 1u)) {
-                        timed_out();
-                        break;
+                    if (!kI8WaitTest) {
+                        const uint32_t bar = cluster_addr(&sm.full[s], 0);
+                        i8_tma_load<true>(sm.st[s], &xmap, kb * I8_KC, m0, bar);
+                        i8_tma_load<true>(sm.st[s] + 128 * I8_KC, wmap, kb * I8_KC, n0, bar);
                     }
+                }
+                if (kI8WaitTest) break;   // armed, no copy
+                if (++s == S) { s = 0; ph ^= 1u; }
+            }
+            if (kI8WaitTest) break;
         }
+        // the releases of the last stages arrive before the CTA ends
+        for (int i = max(0, armed - S); !kI8WaitTest && ok && i < armed; ++i)
+            ok = i8_wait_warp(&sm.empty[i % S], (uint32_t)(i / S) & 1u);
+        if (!ok && issuer) timed_out();
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -221,9 +221,9 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     }
     __syncthreads();
     if (sm.abort_flag) {
-        if (warp == 0 && lane == 0 && rank == 0)
+        if (warp == 0 && rank == 0)
             for (int i = max(0, armed - S); i < armed; ++i)
-                i8_wait(&sm.full[i % S], (uint32_t)(i / S) & 1u);
+                i8_wait_warp(&sm.full[i % S], (uint32_t)(i / S) & 1u);
         if (warp == 1 && rank == 0) {   // every MMA issued so far
             if (elect_one()) i8_commit<true>(&sm.drain);
             i8_wait_warp(&sm.drain, 0u);
