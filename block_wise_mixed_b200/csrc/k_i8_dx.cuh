@@ -9,7 +9,7 @@
 //
 // The codes lie with k along the rows and the contraction across them; the
 // operand wants the contraction along its rows, in bf16.  Twelve warps turn
-// each 64 x 128 code tile (8 KB, by TMA) into the swizzled 128 x 64 operand:
+// each 64 x 128 block of codes (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
 // one byte permute, and makes them bf16 with two masks and one subtraction:
 //   code = bf16(0x4300 | (b & 0x7F)) - bf16(0x4300 | (b & 0x80))
@@ -39,20 +39,24 @@ constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
 
 template <int NT>
 struct I8DxCfg {
-    static constexpr int B = NT / 2 * I8X_NC * 2;              // this CTA's tokens
-    // Operand stages, and code stages with what shared memory is left: few
-    // tokens wait for the codes, many for the operands.
-    static constexpr int S = 5;
-    static constexpr int R = NT == 256 ? 6 : NT == 128 ? 10 : NT == 64 ? 12 : 14;
+    // 64-channel blocks in a stage: two while the codes' bytes bound the time
+    // (a stage's waits, commit and copies cost each role some 400 cycles,
+    // more than the 350 that 8 KB of codes take to arrive), one where the
+    // products do and shared memory is needed for tokens.
+    static constexpr int U = NT == 256 ? 1 : 2;
+    static constexpr int B = NT / 2 * I8X_NC * 2;              // this CTA's tokens, one block
+    static constexpr int B_STRIDE = (B + 1023) / 1024 * 1024;
+    static constexpr int S = NT == 256 ? 5 : 3;                // operand stages
+    static constexpr int R = NT == 256 ? 6 : NT == 128 ? 3 : NT == 64 ? 5 : 6;   // code stages
     static constexpr uint32_t COLS = 2 * NT;                   // double-buffered accumulator
 };
 
 template <int NT>
 struct I8DxSmem {
     using Cfg = I8DxCfg<NT>;
-    uint8_t a[Cfg::S][I8X_A];               // 1024-aligned
-    uint8_t b[Cfg::S][(Cfg::B + 1023) / 1024 * 1024];
-    uint8_t raw[Cfg::R][I8X_RAW];
+    uint8_t a[Cfg::S][Cfg::U * I8X_A];      // 1024-aligned
+    uint8_t b[Cfg::S][Cfg::U * Cfg::B_STRIDE];
+    uint8_t raw[Cfg::R][Cfg::U * I8X_RAW];
     uint64_t raw_full[Cfg::R], raw_empty[Cfg::R];
     uint64_t full[Cfg::S], empty[Cfg::S];   // full: both operands of the pair, in the first CTA
     uint64_t d_full[2], d_empty[2], drain;
@@ -81,8 +85,7 @@ struct I8DxPlace {
         j = c / NB;
         n = c - j * NB;
     }
-    __device__ __forceinline__ void next(int C, int NB, int64_t TM) {
-        if (++n < NB) return;
+    __device__ __forceinline__ void next_matrix(int C, int NB, int64_t TM) {
         n = 0;
         if (++j * NB < C) return;
         j = 0;
@@ -106,7 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8X_WARPS * 32, 1)
 k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
         const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p) {
     using Cfg = I8DxCfg<NT>;
-    constexpr int S = Cfg::S, R = Cfg::R;
+    constexpr int S = Cfg::S, R = Cfg::R, U = Cfg::U;
     static_assert(R >= S && S >= I8X_GROUPS, "the converters' parity waits");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -114,7 +117,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
 
-    const int NB = (p.N + I8X_NC - 1) / I8X_NC, C = NB * p.nw;
+    const int NB = (p.N + U * I8X_NC - 1) / (U * I8X_NC), C = NB * p.nw;
     const int64_t TK = (p.K + 255) / 256, TM = (p.M + NT - 1) / NT;
     const int64_t units = TK * TM * C, G = gridDim.x >> 1, pair = blockIdx.x >> 1;
     const int64_t u0 = i8_run_start(pair, units, G), u1 = i8_run_start(pair + 1, units, G);
@@ -159,38 +162,57 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         int r = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (int64_t u = u0; u < u1; ++u, at.next(C, NB, TM)) {
-            ok = i8_wait_warp(&sm.raw_empty[r], ph);
-            if (!ok) break;
-            ++armed;
-            if (issuer) {
-                mbar_arrive_expect_tx(&sm.raw_full[r], I8X_RAW);
-                if (!kI8WaitTest)
-                    i8_tma_load<false>(sm.raw[r], at.j ? &wmap1 : &wmap0, at.tk * 256 + (int)rank * 128, at.n * I8X_NC,
-                                       smem_u32(&sm.raw_full[r]));
+        int64_t left = u1 - u0;
+        while (left > 0 && ok) {   // along the channels of one matrix
+            const int n = (int)min(left, (int64_t)(NB - at.n));
+            const CUtensorMap* map = at.j ? &wmap1 : &wmap0;
+            const int k0 = at.tk * 256 + (int)rank * 128;
+            int n0 = at.n * U * I8X_NC;
+            for (int i = 0; i < n; ++i, n0 += U * I8X_NC) {
+                ok = i8_wait_warp(&sm.raw_empty[r], ph);
+                if (!ok) break;
+                if (issuer) {
+                    mbar_arrive_expect_tx(&sm.raw_full[r], U * I8X_RAW);
+                    if (!kI8WaitTest) i8_tma_load<false>(sm.raw[r], map, k0, n0, smem_u32(&sm.raw_full[r]));
+                }
+                ++armed;
+                if (kI8WaitTest) break;   // armed, no copy
+                if (++r == R) { r = 0; ph ^= 1u; }
             }
-            if (kI8WaitTest) break;   // armed, no copy
-            if (++r == R) { r = 0; ph ^= 1u; }
+            if (kI8WaitTest) break;
+            left -= n;
+            at.next_matrix(C, NB, TM);
         }
         if (!ok && issuer) timed_out();
         __syncwarp();
     } else if (warp == I8X_WARPS - 1) {
         const bool issuer = elect_one();
         I8DxPlace at(u0, C, NB, TM);
+        const uint32_t full0 = cluster_addr(&sm.full[0], 0);
         int s = 0;
         uint32_t ph = 1;
         bool ok = !kI8WaitTest;
-        for (int64_t u = u0; u < u1 && ok; ++u, at.next(C, NB, TM)) {
-            ok = i8_wait_warp(&sm.empty[s], ph);
-            if (!ok) break;
-            ++armed;
-            if (issuer) {
-                // the first CTA's barrier counts both CTAs' bytes
-                if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Cfg::B);
-                i8_tma_load<true>(sm.b[s], at.j ? &gmap1 : &gmap0, at.n * I8X_NC, at.tm * NT + (int)rank * (NT / 2),
-                                  cluster_addr(&sm.full[s], 0));
+        int64_t left = u1 - u0;
+        while (left > 0 && ok) {
+            const int n = (int)min(left, (int64_t)(NB - at.n));
+            const CUtensorMap* map = at.j ? &gmap1 : &gmap0;
+            const int m0 = at.tm * NT + (int)rank * (NT / 2);
+            int n0 = at.n * U * I8X_NC;
+            for (int i = 0; i < n; ++i, n0 += U * I8X_NC) {
+                ok = i8_wait_warp(&sm.empty[s], ph);
+                if (!ok) break;
+                if (issuer) {
+                    // the first CTA's barrier counts both CTAs' bytes
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * U * Cfg::B);
+#pragma unroll
+                    for (int b = 0; b < U; ++b)
+                        i8_tma_load<true>(sm.b[s] + b * Cfg::B_STRIDE, map, n0 + b * I8X_NC, m0, full0 + 8u * (uint32_t)s);
+                }
+                ++armed;
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (++s == S) { s = 0; ph ^= 1u; }
+            left -= n;
+            at.next_matrix(C, NB, TM);
         }
         // the releases of the last stages arrive before the CTA ends
         for (int i = max(0, armed - S); ok && i < armed; ++i)
@@ -217,7 +239,10 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                     i8_fence_after();
                     const uint32_t a = smem_u32(sm.a[s]), b = smem_u32(sm.b[s]);
                     if (issuer) {
-                        i8_mma4<true, 1>(tmem + (uint32_t)(buf * NT), a, b, idesc, i > 0);
+#pragma unroll
+                        for (int q = 0; q < U; ++q)
+                            i8_mma4<true, 1>(tmem + (uint32_t)(buf * NT), a + q * I8X_A, b + q * Cfg::B_STRIDE, idesc,
+                                             i > 0 || q > 0);
                         i8_commit<true>(&sm.empty[s]);
                         if (i == n - 1) i8_commit<true>(&sm.d_full[buf]);
                     }
@@ -335,42 +360,48 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             const uint32_t row = (uint32_t)(4 * kg + j);
             at[j] = (row >> 3) * 1024 + (row & 7) * 128 + (((uint32_t)c ^ (row & 7)) << 4);
         }
+        const uint32_t full0 = cluster_addr(&sm.full[0], 0);
         const uint32_t n_units = (uint32_t)(u1 - u0);   // a CTA's run: far below 2^32
+        // stage and phase of this group's unit in either ring
+        uint32_t r = group, s = group, rph = 0, sph = 1;
         for (uint32_t it = group; it < n_units; it += I8X_GROUPS) {
-            const uint32_t r = it % R, s = it % S;
             // The operand stage first: a parity wait can tell a phase only from
             // its neighbour.  Units up to it - S are multiplied once empty[s]
             // says so, so (R >= S) the copy of unit it - R has landed and
             // raw_full[r] is at most one phase behind; asked the other way
             // round, that copy (another group's unit) may still be in flight
             // and the wait would pass a phase early.
-            bool ok = !sm.abort_flag && i8_wait(&sm.empty[s], ((it / S) & 1u) ^ 1u);
-            ok = ok && i8_wait(&sm.raw_full[r], (it / R) & 1u);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                if (lane == 0 && !sm.abort_flag) timed_out();
+            if (!i8_wait_warp(&sm.empty[s], sph) || !i8_wait_warp(&sm.raw_full[r], rph)) {
+                if (lane == 0) timed_out();
                 break;
             }
-            uint32_t in[2][8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int b = 0; b < U; ++b) {
+                const uint8_t* raw = sm.raw[r] + b * I8X_RAW + 8 * c * 128 + 4 * kg;
+                uint32_t in[2][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    in[h][i] = *reinterpret_cast<const uint32_t*>(sm.raw[r] + (32 * h + 8 * c + i) * 128 + 4 * kg);
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                    for (int i = 0; i < 8; ++i)
+                        in[h][i] = *reinterpret_cast<const uint32_t*>(raw + (32 * h + i) * 128);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 o = make_uint4(i8_pair_bf16(in[h][0], in[h][1], j), i8_pair_bf16(in[h][2], in[h][3], j),
-                                               i8_pair_bf16(in[h][4], in[h][5], j), i8_pair_bf16(in[h][6], in[h][7], j));
-                    *reinterpret_cast<uint4*>(sm.a[s] + (at[j] ^ (uint32_t)(64 * h))) = o;
-                }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4*>(sm.a[s] + b * I8X_A + (at[j] ^ (uint32_t)(64 * h))) =
+                            make_uint4(i8_pair_bf16(in[h][0], in[h][1], j), i8_pair_bf16(in[h][2], in[h][3], j),
+                                       i8_pair_bf16(in[h][4], in[h][5], j), i8_pair_bf16(in[h][6], in[h][7], j));
+            }
             fence_proxy_async_smem();   // to the tensor cores
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.raw_empty[r]);
-                cluster_arrive(cluster_addr(&sm.full[s], 0));
+                cluster_arrive(full0 + 8u * s);
             }
+            r += I8X_GROUPS;
+            if (r >= R) { r -= R; rph ^= 1u; }
+            s += I8X_GROUPS;
+            if (s >= S) { s -= S; sph ^= 1u; }
         }
     }
     __syncthreads();

@@ -170,7 +170,7 @@ inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K, int nw) {
     return std::min<int64_t>({(int64_t)kSMs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, stream_nt(M)) * nw)});
 }
 inline int64_t dx_pairs(int64_t M, int64_t N, int64_t K, int nw) {
-    const int64_t chunks = div_up(N, I8X_NC) * nw, tiles = div_up(M, dx_nt(M)) * div_up(K, 256);
+    const int64_t chunks = div_up(N, I8X_NC * (dx_nt(M) == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U)) * nw, tiles = div_up(M, dx_nt(M)) * div_up(K, 256);
     return std::min<int64_t>({(int64_t)kPairs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, dx_nt(M)))});
 }
 
@@ -319,7 +319,7 @@ template <int NT>
 mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, I8DxParams& p,
                   void* stream) {
     CUtensorMap w0, w1, g0, g1;
-    if (!make_map(&w0, w[0], I8X_NC, false) || !make_map(&w1, w[nw - 1], I8X_NC, false) ||
+    if (!make_map(&w0, w[0], I8DxCfg<NT>::U * I8X_NC, false) || !make_map(&w1, w[nw - 1], I8DxCfg<NT>::U * I8X_NC, false) ||
         !make_map(&g0, g, true, p.M, p.N, ldg * 2, NT / 2, true) ||
         !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
