@@ -420,50 +420,48 @@ _ACTS = {ACT_SILU: 0, ACT_GELU_TANH: 1}   # mpq_act
 I8_MAX_COLS = 131071                      # MPQ_I8_MAX_COLS
 
 
-@dataclass
 class I8Matrix:
     """An int8 matrix in device memory: codes (int8, rows x cols, rows a
     multiple of 16 bytes apart) and scales (fp32, one a row), plus its C view."""
-    codes: object
-    scales: object
-    c: I8
+    __slots__ = ("codes", "scales", "rows", "cols", "device", "c", "ref")
 
-    @property
-    def rows(self):
-        return self.c.rows
-
-    @property
-    def cols(self):
-        return self.c.cols
+    def __init__(self, codes, scales, ld: int):
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.rows, self.cols = codes.shape
+        self.c = I8(self.rows, self.cols, ld, codes.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
-def _need(ok, where, what):
-    if not ok:
-        raise MpqError(1, "%s: %s" % (where, what))
+def _bad(where, what, status=1):
+    raise MpqError(status, "%s: %s" % (where, what))
 
 
 def _tensor_2d(t, where, name, dtypes, device=None, shape=None):
     """Checks a 2-D CUDA tensor argument with unit column stride; returns its
     row stride in elements."""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dim() == 2, where, "%s must be a 2-D tensor" % name)
-    _need(t.dtype in dtypes, where, "%s has dtype %s" % (name, t.dtype))
-    _need(t.is_cuda, where, "%s must be on a CUDA device" % name)
-    _need(device is None or t.device == device, where, "%s is on another device" % name)
-    _need(shape is None or tuple(t.shape) == tuple(shape), where,
-          "%s is %s, not %s" % (name, tuple(t.shape), shape))
-    rows, cols = t.shape
+    if not isinstance(t, torch.Tensor):
+        _bad(where, "%s must be a tensor" % name)
+    if t.dtype not in dtypes:
+        _bad(where, "%s has dtype %s" % (name, t.dtype))
+    shp = t.shape
+    if len(shp) != 2:
+        _bad(where, "%s must have two dimensions" % name)
+    if not t.is_cuda:
+        _bad(where, "%s must be on a CUDA device" % name)
+    if device is not None and t.device != device:
+        _bad(where, "%s is on another device" % name)
+    rows, cols = shp
+    if shape is not None and (rows != shape[0] or cols != shape[1]):
+        _bad(where, "%s is %s, not %s" % (name, tuple(shp), tuple(shape)))
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        _bad(where, "%s must have unit column stride" % name)
     if rows > 1:
-        _need((cols <= 1 or t.stride(1) == 1) and t.stride(0) >= cols, where,
-              "%s must have unit column stride and rows that do not overlap" % name)
-        return t.stride(0)
-    _need(cols <= 1 or t.stride(1) == 1, where, "%s must have unit column stride" % name)
-    return max(cols, 1)
-
-
-def _ydt(t):
-    import torch
-    return Y_BF16 if t.dtype == torch.bfloat16 else Y_F32
+        if s0 < cols:
+            _bad(where, "rows of %s overlap" % name)
+        return s0
+    return cols if cols > 0 else 1
 
 
 def i8_matrix(codes, scales) -> I8Matrix:
@@ -474,10 +472,12 @@ def i8_matrix(codes, scales) -> I8Matrix:
     rows, cols = codes.shape
     if rows <= 1:
         ld = (cols + 15) // 16 * 16
-    _need(ld % 16 == 0 and codes.data_ptr() % 16 == 0, "i8_matrix", "rows of codes must be 16-byte aligned")
-    _need(scales.dtype == torch.float32 and scales.device == codes.device and scales.is_contiguous()
-          and tuple(scales.shape) == (rows,), "i8_matrix", "scales must be %d contiguous floats" % rows)
-    return I8Matrix(codes, scales, I8(rows, cols, ld, codes.data_ptr(), scales.data_ptr()))
+    if ld % 16 or codes.data_ptr() % 16:
+        _bad("i8_matrix", "rows of codes must be 16-byte aligned")
+    if not (isinstance(scales, torch.Tensor) and scales.dtype == torch.float32 and scales.device == codes.device
+            and scales.is_contiguous() and tuple(scales.shape) == (rows,)):
+        _bad("i8_matrix", "scales must be %d contiguous floats on the codes' device" % rows)
+    return I8Matrix(codes, scales, ld)
 
 
 def i8_empty(rows: int, cols: int, device) -> I8Matrix:
@@ -487,49 +487,64 @@ def i8_empty(rows: int, cols: int, device) -> I8Matrix:
     return i8_matrix(codes, torch.empty(rows, dtype=torch.float32, device=device))
 
 
-def _i8_mat(q, where, name, device=None, cols=None):
-    _need(isinstance(q, I8Matrix), where, "%s must be an I8Matrix" % name)
-    _need(device is None or q.codes.device == device, where, "%s is on another device" % name)
+def _mat(q, where, name, device=None, cols=None):
+    if q.__class__ is not I8Matrix:
+        _bad(where, "%s must be an I8Matrix" % name)
+    if device is not None and q.device != device:
+        _bad(where, "%s is on another device" % name)
     if cols is not None and q.cols != cols:
-        raise MpqError(2, "%s: %s has %d columns, not %d" % (where, name, q.cols, cols))
-    return q
+        _bad(where, "%s has %d columns, not %d" % (name, q.cols, cols), 2)
+    return q.device
 
 
-def _on(device, stream):
-    """The device guard and stream handle of a call on tensors of `device`."""
+def _new(shape, dtype, device, stream, zero=False):
+    """A tensor for a call on `stream` (None: the current one), allocated on
+    the current stream: the call waits for the memory's earlier uses (and the
+    zero fill), and the memory is not reused before the call is done."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    _need(s.device == device, "stream", "the stream is on another device than the tensors")
-    return torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
-
-
-def _i8_ws(ws, size, device, where):
-    import torch
-    if ws is None:
-        return torch.zeros(size, dtype=torch.uint8, device=device)
-    _need(ws.is_cuda and ws.device == device and ws.is_contiguous(), where, "ws is not contiguous on the device")
-    return ws
-
-
-def _i8_call(name, device, stream, ws, size, *args):
-    guard, s = _on(device, stream)
-    with guard:
-        w = _i8_ws(ws, size, device, name)
-        if stream is not None and ws is None:
-            w.record_stream(stream)      # allocated here, used on the caller's stream
-            import torch
-            stream.wait_stream(torch.cuda.current_stream(device))   # its zero fill
-        _raise(getattr(lib(), name)(*args, w.data_ptr(), w.numel() * w.element_size(), s), name)
+    t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+        stream.wait_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _out(out, shape, device, where, name, dtypes, stream):
-    import torch
     if out is None:
-        out = torch.empty(shape, dtype=dtypes[0], device=device)
-        if stream is not None:
-            out.record_stream(stream)
-            stream.wait_stream(torch.cuda.current_stream(device))   # the memory's earlier uses
+        return _new(shape, dtypes[0], device, stream), max(shape[1], 1)
     return out, _tensor_2d(out, where, name, dtypes, device, shape)
+
+
+def _call(name, device, stream, *args):
+    """Calls the library on `stream` (None: the current one) of `device`, with
+    that device current."""
+    import torch
+    idx = device.index
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(idx)
+    else:
+        if stream.device != device:
+            _bad(name, "the stream is on another device than the tensors")
+        s = stream.cuda_stream
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == idx:
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st:
+        raise MpqError(st, name)
+
+
+def _call_ws(name, sizes, device, stream, ws, *args):
+    """_call with a workspace: the caller's, or a new zeroed one of the size
+    that `name` asks for at `sizes`."""
+    import torch
+    if ws is None:
+        ws = _new((getattr(lib(), name + "_workspace_size")(*sizes),), torch.uint8, device, stream, zero=True)
+    elif not (isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == device):
+        _bad(name, "ws must be a contiguous tensor on the device of the others")
+    _call(name, device, stream, *args, ws.data_ptr(), ws.nbytes)
 
 
 def i8_quantize(x, out: I8Matrix = None, stream=None) -> I8Matrix:
@@ -537,30 +552,33 @@ def i8_quantize(x, out: I8Matrix = None, stream=None) -> I8Matrix:
     scale a row."""
     import torch
     ldx = _tensor_2d(x, "i8_quantize", "x", (torch.bfloat16, torch.float32))
+    rows, cols = x.shape
+    dev = x.device
     if out is None:
-        out = i8_empty(x.shape[0], x.shape[1], x.device)
-        if stream is not None:
-            for t in (out.codes, out.scales):
-                t.record_stream(stream)
-            stream.wait_stream(torch.cuda.current_stream(x.device))
-    _i8_mat(out, "i8_quantize", "out", x.device, x.shape[1])
-    _need(out.rows == x.shape[0], "i8_quantize", "out has %d rows, not %d" % (out.rows, x.shape[0]))
-    guard, s = _on(x.device, stream)
-    with guard:
-        _raise(lib().mpq_i8_quantize(x.data_ptr(), _ydt(x), ldx, ctypes.byref(out.c), s), "mpq_i8_quantize")
+        out = I8Matrix(_new((rows, (cols + 15) // 16 * 16), torch.int8, dev, stream)[:, :cols],
+                       _new((rows,), torch.float32, dev, stream), (cols + 15) // 16 * 16)
+    _mat(out, "i8_quantize", "out", dev, cols)
+    if out.rows != rows:
+        _bad("i8_quantize", "out has %d rows, not %d" % (out.rows, rows))
+    _call("mpq_i8_quantize", dev, stream, x.data_ptr(), Y_BF16 if x.dtype is torch.bfloat16 else Y_F32, ldx, out.ref)
     return out
+
+
+def _dtypes(ydtype):
+    import torch
+    return (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
+
+
+def _ydt(t):
+    import torch
+    return Y_BF16 if t.dtype is torch.bfloat16 else Y_F32
 
 
 def i8_dequantize(q: I8Matrix, out=None, stream=None, ydtype: int = Y_F32):
     """mpq_i8_dequantize: codes * scales in fp32, or bf16 (out's type, or ydtype)."""
-    import torch
-    _i8_mat(q, "i8_dequantize", "q")
-    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
-    dev = q.codes.device
-    out, ld = _out(out, (q.rows, q.cols), dev, "i8_dequantize", "out", dts, stream)
-    guard, s = _on(dev, stream)
-    with guard:
-        _raise(lib().mpq_i8_dequantize(ctypes.byref(q.c), out.data_ptr(), _ydt(out), ld, s), "mpq_i8_dequantize")
+    dev = _mat(q, "i8_dequantize", "q")
+    out, ld = _out(out, (q.rows, q.cols), dev, "i8_dequantize", "out", _dtypes(ydtype), stream)
+    _call("mpq_i8_dequantize", dev, stream, q.ref, out.data_ptr(), _ydt(out), ld)
     return out
 
 
@@ -582,18 +600,16 @@ def i8_gated_backward_workspace_size(M: int, F: int, K: int) -> int:
 
 def i8_linear(x: I8Matrix, w: I8Matrix, out=None, ws=None, stream=None, ydtype: int = Y_F32):
     """mpq_i8_linear: y (M x N, fp32 or bf16: out's type, or ydtype) = x_hat * w_hat^T."""
-    import torch
-    dev = _i8_mat(x, "i8_linear", "x").codes.device
-    _i8_mat(w, "i8_linear", "w", dev, x.cols)
-    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
-    out, ld = _out(out, (x.rows, w.rows), dev, "i8_linear", "out", dts, stream)
-    _i8_call("mpq_i8_linear", dev, stream, ws, i8_linear_workspace_size(x.rows, w.rows, x.cols),
-             ctypes.byref(x.c), ctypes.byref(w.c), out.data_ptr(), _ydt(out), ld)
+    dev = _mat(x, "i8_linear", "x")
+    _mat(w, "i8_linear", "w", dev, x.cols)
+    out, ld = _out(out, (x.rows, w.rows), dev, "i8_linear", "out", _dtypes(ydtype), stream)
+    _call_ws("mpq_i8_linear", (x.rows, w.rows, x.cols), dev, stream, ws, x.ref, w.ref, out.data_ptr(), _ydt(out), ld)
     return out
 
 
 def _act(act, where):
-    _need(act in _ACTS, where, "act must be one of %s" % sorted(_ACTS))
+    if act not in _ACTS:
+        _bad(where, "act must be one of %s" % sorted(_ACTS))
     return _ACTS[act]
 
 
@@ -601,30 +617,27 @@ def i8_gated(x: I8Matrix, w_gate: I8Matrix, w_up: I8Matrix, act: str = ACT_SILU,
              stream=None, ydtype: int = Y_BF16):
     """mpq_i8_gated: h (M x F, bf16 or fp32: out's type, or ydtype) =
     act(x_hat * w_gate_hat^T) * (x_hat * w_up_hat^T)."""
-    import torch
-    dev = _i8_mat(x, "i8_gated", "x").codes.device
-    for n, w in (("w_gate", w_gate), ("w_up", w_up)):
-        _i8_mat(w, "i8_gated", n, dev, x.cols)
-    dts = (torch.bfloat16, torch.float32) if ydtype == Y_BF16 else (torch.float32, torch.bfloat16)
-    out, ld = _out(out, (x.rows, w_gate.rows), dev, "i8_gated", "out", dts, stream)
-    _i8_call("mpq_i8_gated", dev, stream, ws, i8_gated_workspace_size(x.rows, w_gate.rows, x.cols),
-             ctypes.byref(x.c), ctypes.byref(w_gate.c), ctypes.byref(w_up.c), _act(act, "i8_gated"),
-             out.data_ptr(), _ydt(out), ld)
+    dev = _mat(x, "i8_gated", "x")
+    _mat(w_gate, "i8_gated", "w_gate", dev, x.cols)
+    _mat(w_up, "i8_gated", "w_up", dev, x.cols)
+    out, ld = _out(out, (x.rows, w_gate.rows), dev, "i8_gated", "out", _dtypes(ydtype), stream)
+    _call_ws("mpq_i8_gated", (x.rows, w_gate.rows, x.cols), dev, stream, ws, x.ref, w_gate.ref, w_up.ref,
+             _act(act, "i8_gated"), out.data_ptr(), _ydt(out), ld)
     return out
 
 
 def i8_linear_backward(w: I8Matrix, dy, out=None, ws=None, stream=None):
     """mpq_i8_linear_backward: dx (bf16, M x K) = dy (bf16, M x N) * w_hat."""
     import torch
-    bf = (torch.bfloat16,)
-    dev = _i8_mat(w, "i8_linear_backward", "w").codes.device
-    lddy = _tensor_2d(dy, "i8_linear_backward", "dy", bf, dev)
-    if dy.shape[1] != w.rows:
-        raise MpqError(2, "i8_linear_backward: dy has %d columns, not %d" % (dy.shape[1], w.rows))
-    out, ld = _out(out, (dy.shape[0], w.cols), dev, "i8_linear_backward", "out", bf, stream)
-    _i8_call("mpq_i8_linear_backward", dev, stream, ws,
-             i8_linear_backward_workspace_size(dy.shape[0], w.rows, w.cols),
-             ctypes.byref(w.c), dy.data_ptr(), dy.shape[0], lddy, out.data_ptr(), ld)
+    where, bf = "i8_linear_backward", (torch.bfloat16,)
+    dev = _mat(w, where, "w")
+    lddy = _tensor_2d(dy, where, "dy", bf, dev)
+    M, N = dy.shape
+    if N != w.rows:
+        _bad(where, "dy has %d columns, not %d" % (N, w.rows), 2)
+    out, ld = _out(out, (M, w.cols), dev, where, "out", bf, stream)
+    _call_ws("mpq_i8_linear_backward", (M, N, w.cols), dev, stream, ws, w.ref, dy.data_ptr(), M, lddy,
+             out.data_ptr(), ld)
     return out
 
 
@@ -633,16 +646,16 @@ def i8_gated_backward(x: I8Matrix, w_gate: I8Matrix, w_up: I8Matrix, dh, act: st
     """mpq_i8_gated_backward: (dx, d_gate, d_up), all bf16, from dh (bf16, M x F)."""
     import torch
     where, bf = "i8_gated_backward", (torch.bfloat16,)
-    dev = _i8_mat(x, where, "x").codes.device
-    for n, w in (("w_gate", w_gate), ("w_up", w_up)):
-        _i8_mat(w, where, n, dev, x.cols)
+    dev = _mat(x, where, "x")
+    _mat(w_gate, where, "w_gate", dev, x.cols)
+    _mat(w_up, where, "w_up", dev, x.cols)
     M, F = x.rows, w_gate.rows
     lddh = _tensor_2d(dh, where, "dh", bf, dev, (M, F))
     dx, lddx = _out(dx, (M, x.cols), dev, where, "dx", bf, stream)
     d_gate, ldg = _out(d_gate, (M, F), dev, where, "d_gate", bf, stream)
     d_up, ldu = _out(d_up, (M, F), dev, where, "d_up", bf, stream)
-    _need(ldg == ldu, where, "d_gate and d_up must have the same row stride")
-    _i8_call("mpq_i8_gated_backward", dev, stream, ws, i8_gated_backward_workspace_size(M, F, x.cols),
-             ctypes.byref(x.c), ctypes.byref(w_gate.c), ctypes.byref(w_up.c), _act(act, where), dh.data_ptr(),
-             lddh, d_gate.data_ptr(), d_up.data_ptr(), ldg, dx.data_ptr(), lddx)
+    if ldg != ldu:
+        _bad(where, "d_gate and d_up must have the same row stride")
+    _call_ws("mpq_i8_gated_backward", (M, F, x.cols), dev, stream, ws, x.ref, w_gate.ref, w_up.ref,
+             _act(act, where), dh.data_ptr(), lddh, d_gate.data_ptr(), d_up.data_ptr(), ldg, dx.data_ptr(), lddx)
     return dx, d_gate, d_up

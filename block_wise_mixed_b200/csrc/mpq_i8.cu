@@ -21,6 +21,8 @@ using namespace mpq;
 
 namespace {
 
+constexpr int kSMs = 148;
+
 inline size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -69,19 +71,31 @@ mpq_status launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
 // ---------------------------------------------------------------------------
 // rows
 // ---------------------------------------------------------------------------
-template <bool BF16, bool VEC>
+template <bool BF16, bool SHIFT, int G, int VPT, bool LONG = false>
+mpq_status quantize_run(const I8RowsParams& p, void* stream) {
+    constexpr int threads = G >= 128 ? G : 128;
+    static const int resident = [] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_i8_quantize<BF16, SHIFT, G, VPT, LONG>, threads, 0) ==
+                       cudaSuccess && n > 0 ? n : 1;
+    }();
+    const int64_t blocks = std::min<int64_t>(div_up(p.rows, threads / G), (int64_t)kSMs * resident);
+    return launch(k_i8_quantize<BF16, SHIFT, G, VPT, LONG>, dim3((unsigned)blocks), threads, 0, stream, p);
+}
+
+// Threads a row: as few as hold it in four 16-byte blocks each (rows of 1000
+// bf16: 4.3 us for 4096 of them, 7.0 with eight), eight from 32 KB on; for a few
+// rows, as many as have a block to load.
+template <bool BF16, bool SHIFT>
 mpq_status quantize_launch(const I8RowsParams& p, void* stream) {
-    constexpr int PER = VEC ? I8Elem<BF16>::PER : 1;
-    constexpr int VPT = VEC ? 8 : 32;   // loads kept by a thread (32 registers)
-    const int64_t units = p.cols / PER;
-    // a few rows: as many threads a row as have a load to make
-    const bool few = p.rows <= 148;
-    if (units > 512 * VPT) return launch(k_i8_quantize<BF16, VEC, 512, VPT, true>, dim3(p.rows), 512, 0, stream, p);
-    if (units > 128 * VPT || (few && units > 128))
-        return launch(k_i8_quantize<BF16, VEC, 512, VPT, false>, dim3(p.rows), 512, 0, stream, p);
-    if (units > 32 * VPT || (few && units > 32))
-        return launch(k_i8_quantize<BF16, VEC, 128, VPT, false>, dim3(p.rows), 128, 0, stream, p);
-    return launch(k_i8_quantize<BF16, VEC, 32, VPT, false>, dim3((unsigned)div_up(p.rows, 4)), 128, 0, stream, p);
+    const int64_t warps = div_up(div_up(p.cols, I8Elem<BF16>::PER) + (SHIFT ? 1 : 0), SHIFT ? 31 : 32);
+    const int64_t per = p.rows <= kSMs ? 1 : 4;
+    if (warps > 16 * 8) return quantize_run<BF16, SHIFT, 512, 8, true>(p, stream);
+    if (warps > 16 * 4) return quantize_run<BF16, SHIFT, 512, 8>(p, stream);
+    if (warps > 8 * per) return quantize_run<BF16, SHIFT, 512, 4>(p, stream);
+    if (warps > 4 * per) return quantize_run<BF16, SHIFT, 256, 4>(p, stream);
+    if (warps > per) return quantize_run<BF16, SHIFT, 128, 4>(p, stream);
+    return quantize_run<BF16, SHIFT, 32, 4>(p, stream);
 }
 
 }  // namespace
@@ -104,9 +118,10 @@ mpq_status mpq_i8_quantize(const void* x_dev, mpq_ydtype dt, int64_t ldx, const 
     p.ldc = out->ld;
     p.rows = out->rows;
     p.cols = out->cols;
-    const bool vec = aligned(x_dev, 16) && (out->rows == 1 || ldx * (int64_t)es % 16 == 0);
-    if (dt == MPQ_Y_BF16) return vec ? quantize_launch<true, true>(p, stream) : quantize_launch<true, false>(p, stream);
-    return vec ? quantize_launch<false, true>(p, stream) : quantize_launch<false, false>(p, stream);
+    const bool vec = aligned(x_dev, 16) && (out->rows == 1 || ldx * (int64_t)es % 16 == 0) &&
+                     out->cols * (int64_t)es % 16 == 0;   // rows are whole 16-byte blocks
+    if (dt == MPQ_Y_BF16) return vec ? quantize_launch<true, false>(p, stream) : quantize_launch<true, true>(p, stream);
+    return vec ? quantize_launch<false, false>(p, stream) : quantize_launch<false, true>(p, stream);
 }
 
 mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_t ldx, void* stream) {
@@ -126,8 +141,8 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
     p.rows = q->rows;
     p.cols = q->cols;
     const bool vec = aligned(x_dev, 16) && (q->rows == 1 || ldx * (int64_t)es % 16 == 0);
-    const int64_t per = 256 * (vec ? 16 * 2 : 8);
-    const dim3 grid((unsigned)q->rows, (unsigned)div_up(q->cols, q->rows <= 148 ? per / (vec ? 2 : 8) : per));
+    const int64_t per = 256 * (vec ? 4 * 16 / (int64_t)es : 32);   // a block's columns in one round
+    const dim3 grid((unsigned)q->rows, (unsigned)div_up(q->cols, per));
     if (dt == MPQ_Y_BF16) return vec ? launch(k_i8_dequantize<true, true>, grid, 256, 0, stream, p)
                                      : launch(k_i8_dequantize<true, false>, grid, 256, 0, stream, p);
     return vec ? launch(k_i8_dequantize<false, true>, grid, 256, 0, stream, p)
@@ -138,7 +153,6 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
 
 namespace {
 
-constexpr int kSMs = 148;
 constexpr int kPairs = kSMs / 2;
 // Up to here the weights' bytes bound a product and k_i8_stream takes it;
 // above, k_i8_tile.
