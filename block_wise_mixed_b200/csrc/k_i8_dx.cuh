@@ -8,7 +8,7 @@
 // tokens over the two SMs of a cluster.
 //
 // The codes lie with k along the rows and the contraction across them; the
-// operand wants the contraction along its rows, in bf16.  Twelve warps turn
+// operand wants the contraction along its rows, in bf16.  Eight warps turn
 // each 64 x 128 block of codes (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
 // one byte permute, and makes them bf16 with two masks and one subtraction:
@@ -21,8 +21,8 @@
 // fp32 partial sums of a cut tile are added in the order of the runs by the
 // last contributor, whoever that is, so results are reproducible.
 //
-// Roles: warp 0 copies, warp 1 of the first CTA issues, warps 2-5 finish
-// (lane = k column), warps 6-13 convert.  Every wait is bounded.
+// Roles: warp 0 copies, warp 1 of the first CTA issues, warps 2-9 finish
+// (lane = k column), warps 10-17 convert.  Every wait is bounded.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -30,9 +30,10 @@
 
 namespace mpq {
 
-constexpr int I8X_GROUPS = 3;               // converter groups, a stage each in turn
+constexpr int I8X_GROUPS = 2;               // converter groups, a stage each in turn
 constexpr int I8X_GWARPS = 4;               // warps of a group
-constexpr int I8X_WARPS = 7 + I8X_GROUPS * I8X_GWARPS;
+constexpr int I8X_EPI = 8;                  // two for each TMEM lane quadrant
+constexpr int I8X_WARPS = 3 + I8X_EPI + I8X_GROUPS * I8X_GWARPS;
 constexpr int I8X_NC = 64;                  // channels in a stage
 constexpr int I8X_RAW = I8X_NC * 128;       // codes of a stage
 constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
@@ -133,7 +134,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.d_full[b], 1);
-            mbar_init(&sm.d_empty[b], 8);
+            mbar_init(&sm.d_empty[b], 2 * I8X_EPI);
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
@@ -257,8 +258,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             if (!ok && issuer) timed_out();
         }
         __syncwarp();
-    } else if (warp < 6) {
-        const int quad = warp & 3;
+    } else if (warp < 2 + I8X_EPI) {
+        const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 64
         const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
         int seg = 0;
         for (int64_t u = u0; u < u1; ++seg) {
@@ -282,15 +283,15 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             // A cut tile: when all others have arrived already (the usual case
             // for the run that holds the tile's start, its last work), this
             // one only adds; else it leaves its part and counts itself in.
-            uint32_t* counter = p.counters + (c0 * 2 + rank) * 4 + quad;
+            uint32_t* counter = p.counters + (c0 * 2 + rank) * I8X_EPI + warp - 2;
             const uint32_t others = (uint32_t)(c1 - c0);
-            bool mine = true;
-            if (c0 != c1) {
+            bool mine = 32 * half < mc;
+            if (mine && c0 != c1) {
                 uint32_t seen = 0;
                 if (lane == 0) seen = i8_load_acquire(counter);
                 if (__shfl_sync(0xffffffffu, seen, 0) != others) {
                     float* slot = slot_of(pair);
-                    for (int c = 0; c < mc; c += 32) {
+                    for (int c = 32 * half; c < mc; c += 64) {
                         uint32_t r[32];
                         i8_tmem_ld32(taddr + (uint32_t)c, r);
                         i8_tmem_wait();
@@ -309,7 +310,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 }
             }
             if (mine) {
-                for (int c = 0; c < mc; c += 32) {
+                for (int c = 32 * half; c < mc; c += 64) {
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -348,11 +349,11 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             u = end;
         }
     } else {
-        // converters: a group takes every third stage, so that three stages'
+        // converters: a group takes every other stage, so that two stages'
         // waits, loads and fences overlap.  Warp q of it takes rows 0 .. 31,
         // then 32 .. 63; lane (c, g) the eight rows of block c and the four
         // columns of group (g + 8 c + 8 q) % 32
-        const int group = (warp - 6) / I8X_GWARPS, q = (warp - 6) % I8X_GWARPS, c = lane & 3;
+        const int group = (warp - 2 - I8X_EPI) / I8X_GWARPS, q = (warp - 2 - I8X_EPI) % I8X_GWARPS, c = lane & 3;
         const int kg = ((lane >> 2) + 8 * c + 8 * q) & 31;
         uint32_t at[4];   // chunk of column 4 kg + j, block c (block c + 4: the other half of the row)
 #pragma unroll

@@ -15,16 +15,20 @@
 // sums are integers, so the result does not depend on the cuts or the order.
 // Gated: gate and up tiles ride in the same stage, against the same tokens.
 //
-// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-5 read the
-// accumulators (one TMEM lane quadrant each).  Every wait is bounded.
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-9 read the
+// accumulators (two for each TMEM lane quadrant, taking alternate groups of 16
+// tokens).  Every wait is bounded.
 #pragma once
+#include <type_traits>
+
 #include "i8_gate.cuh"
 #include "i8_tc.cuh"
 #include "k_i8_rows.cuh"
 
 namespace mpq {
 
-constexpr int I8S_WARPS = 6;
+constexpr int I8S_EPI = 8;                            // two for each TMEM lane quadrant
+constexpr int I8S_WARPS = 2 + I8S_EPI;
 constexpr int I8S_MAX_CTAS = 256;                     // counters in the workspace
 constexpr int I8_KC = 128;                            // bytes of k in a stage
 
@@ -158,7 +162,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.d_full[b], 1);
-            mbar_init(&sm.d_empty[b], 4);
+            mbar_init(&sm.d_empty[b], I8S_EPI);
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
@@ -244,12 +248,16 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         if (!ok && issuer) timed_out();
         __syncwarp();
     } else {
-        const int quad = warp & 3;
+        const int quad = warp & 3, half = (warp - 2) >> 2;
         int seg = 0;
         for (int64_t u = u0; u < u1; ++seg) {
             const int64_t tile = u / KB, t0 = tile * KB, t1 = t0 + KB;
             const int64_t end = min(u1, t1);
             const int buf = seg % BUFS;
+            const int n = (int)(tile % T) * 128 + quad * 32 + lane, m0 = (int)(tile / T) * NT;
+            const int mc = min(NT, p.M - m0);
+            const bool in = n < p.N;
+            const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
             bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg / BUFS) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
             if (!ok) {
@@ -257,11 +265,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 break;
             }
             i8_fence_after();
-            const int n = (int)(tile % T) * 128 + quad * 32 + lane, m0 = (int)(tile / T) * NT;
-            const int mc = min(NT, p.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NW * NT);
-            const bool in = n < p.N;
-            const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
             // contributors c0 .. c1; this CTA's slot: 1 for the tile that
             // starts inside its run, 0 for the one that began before it
             const int64_t c0 = i8_run_of(t0, units, G), c1 = i8_run_of(t1 - 1, units, G);
@@ -270,15 +274,15 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
-            uint32_t* counter = p.counters + c0 * 4 + quad;
+            uint32_t* counter = p.counters + c0 * I8S_EPI + warp - 2;
             const uint32_t others = (uint32_t)(c1 - c0);
-            bool mine = true;   // this warp writes the results
-            if (c0 != c1) {
+            bool mine = 16 * half < mc;   // this warp writes the results
+            if (mine && c0 != c1) {
                 uint32_t seen = 0;
                 if (lane == 0) seen = i8_load_acquire(counter);
                 if (__shfl_sync(0xffffffffu, seen, 0) != others) {
                     int32_t* slot = slot_of(cta);
-                    for (int c = 0; c < mc; c += 16) {
+                    for (int c = 16 * half; c < mc; c += 32) {
 #pragma unroll
                         for (int j = 0; j < NW; ++j) {
                             uint32_t r[16];
@@ -299,60 +303,65 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     __threadfence();
                 }
             }
-            if (mine) {
-                for (int c = 0; c < mc; c += 16) {
-                    int acc[NW][16];
-                    if (c0 != c1) {
+            // Columns c .. c + CW - 1: the sums, then the outputs.  Loads come
+            // first (a store may alias them for all the compiler knows, and
+            // each would wait for the one before), Q contributors' at a time.
+            auto finish = [&](auto cw, auto qn, int c) {
+                constexpr int CW = decltype(cw)::value, Q = decltype(qn)::value;
+                const int left = mc - c;
+                float xs[CW], dh[MODE == 2 ? CW : 1];
 #pragma unroll
-                        for (int j = 0; j < NW; ++j)
+                for (int i = 0; i < CW; ++i) xs[i] = i < left ? p.xs[m0 + c + i] : 0.f;
+                I8Column<MODE, ACT> col(p, m0 + c, in ? n : 0, ws0, ws1);
+                if (MODE == 2)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[j][i] = 0;
-                        for (int64_t o = c0; o <= c1; o += 2) {   // two contributors' loads in flight
-                            int t[2][NW][16];
+                    for (int i = 0; i < CW; ++i)
+                        if (i < left) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
+                int acc[NW][CW];
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const bool add = o + q <= c1 && o + q != cta;
-                                const int32_t* slot = slot_of(o + q);
+                for (int j = 0; j < NW; ++j) {
+                    uint32_t r[CW];
+                    if (CW == 16) i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
+                    else i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r);
+                    i8_tmem_wait();
 #pragma unroll
-                                for (int j = 0; j < NW; ++j)
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        t[q][j][i] = add && c + i < mc ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
-                            }
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int j = 0; j < NW; ++j)
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) acc[j][i] += t[q][j][i];
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < NW; ++j) {
-                        uint32_t r[16];
-                        i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
-                        i8_tmem_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[j][i] = (c0 != c1 ? acc[j][i] : 0) + (int)r[i];
-                    }
-                    if (in) {
-                        I8Column<MODE, ACT> col(p, m0 + c, n, ws0, ws1);
-                        const float* xs = p.xs + m0 + c;
-                        const int left = mc - c;
-                        float dh[MODE == 2 ? 16 : 1];
-                        if (MODE == 2)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i < left) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < left) {
-                                col.put(acc[0][i], acc[NW - 1][i], xs[i], dh[MODE == 2 ? i : 0]);
-                                col.next();
-                            }
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < CW; ++i) acc[j][i] = (int)r[i];
                 }
+                if (c0 != c1)
+                    for (int64_t o = c0; o <= c1; o += Q) {
+                        int t[Q][NW][CW];
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) {
+                            const bool add = o + q <= c1 && o + q != cta;
+                            const int32_t* slot = slot_of(o + q);
+#pragma unroll
+                            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                for (int i = 0; i < CW; ++i)
+                                    t[q][j][i] = add && i < left ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
+                        }
+#pragma unroll
+                        for (int q = 0; q < Q; ++q)
+#pragma unroll
+                            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                for (int i = 0; i < CW; ++i) acc[j][i] += t[q][j][i];
+                    }
+                if (in) {
+#pragma unroll
+                    for (int i = 0; i < CW; ++i)
+                        if (i < left) {
+                            col.put(acc[0][i], acc[NW - 1][i], xs[i], dh[MODE == 2 ? i : 0]);
+                            col.next();
+                        }
+                }
+                __syncwarp();
+            };
+            if (mine) {
+                if (mc <= 8) finish(std::integral_constant<int, 8>{}, std::integral_constant<int, 4 / NW>{}, 0);
+                else
+                    for (int c = 16 * half; c < mc; c += 32)
+                        finish(std::integral_constant<int, 16>{}, std::integral_constant<int, 2 / NW>{}, c);
             }
             i8_fence_before();
             __syncwarp();

@@ -156,28 +156,43 @@ namespace {
 constexpr int kPairs = kSMs / 2;
 // Up to here the weights' bytes bound a product and k_i8_stream takes it;
 // above, k_i8_tile.
-constexpr int kStreamMaxM = 128;
+#ifndef MAXM
+#define MAXM 128
+#endif
+constexpr int kStreamMaxM = MAXM;
 
 // Workspace: the error word, the counters (zero between calls), then scratch
 // that a call writes before it reads.  The zeroed part has one size for all
 // mpq_i8_* calls, so one workspace serves them all, one after another.
 constexpr size_t kErrBytes = 256;
-constexpr size_t kI8ZeroBytes = kErrBytes + (size_t)kSMs * 4 * 4 + 256 - (size_t)kSMs * 4 * 4 % 256;
+constexpr size_t kI8ZeroBytes = kErrBytes + 5120;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
+static_assert(kSMs * I8S_EPI * 4 <= 5120 && kPairs * 2 * I8X_EPI * 4 <= 5120, "counters");
 
 inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
 }
 
 // Tokens per tile of the streaming kernel, and of the gradient kernel.
+#ifdef FORCE_NT
+inline int stream_nt(int64_t M) { return FORCE_NT; }
+#else
 inline int stream_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+#endif
+#ifdef FORCE_DX
+inline int dx_nt(int64_t M) { return FORCE_DX; }
+#else
 inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
+#endif
+#ifndef CUTK
+#define CUTK 14.0
+#endif
 // Runs that a tile of `chunks` units may be cut into: a unit costs about as
 // long (0.35 us at an SM's share of HBM) as the last contributor takes to add
 // 14 columns of one more partial sum, so n runs cost chunks / n + n cols / 14
 // units, least at n = sqrt(14 chunks / cols).
 inline int64_t max_cuts(int64_t chunks, int64_t cols) {
-    return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(14.0 * (double)chunks / (double)cols)));
+    return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(CUTK * (double)chunks / (double)cols)));
 }
 inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K, int nw) {
     const int64_t chunks = div_up(K, I8_KC), tiles = div_up(M, stream_nt(M)) * div_up(N, 128);
