@@ -17,11 +17,12 @@
 // the 4-byte reads and the 16-byte writes use all banks.  A weight byte
 // crosses HBM once for NT tokens and is never stored wider.
 //
-// Work is cut as in k_i8_stream (equal runs of 64-row units, one a pair); the
-// fp32 partial sums of a cut tile are added in the order of the runs by the
-// last contributor, whoever that is, so results are reproducible.
+// Work is handed to the pairs as in k_i8_stream; the fp32 partial sums of a
+// cut tile are added in the order of the pieces by the last contributor,
+// whoever that is, so results are reproducible.
 //
-// Roles: warp 0 copies, warp 1 of the first CTA issues, warps 2-9 finish
+// Roles: warp 0 copies the codes and warp 18 the tokens, each as far ahead as
+// its own stages allow; warp 1 of the first CTA issues, warps 2-9 finish
 // (lane = k column), warps 10-17 convert.  Every wait is bounded.
 #pragma once
 #include <cuda_bf16.h>
@@ -74,28 +75,6 @@ struct I8DxParams {
     float* slots;
 };
 
-// Where a unit lies: tile (tk, tm), matrix j and its channel block n; counted
-// along, since a 64-bit division a unit would hold the copies up.
-struct I8DxPlace {
-    int tk, tm, j, n;
-    __device__ __forceinline__ I8DxPlace(int64_t u, int C, int NB, int64_t TM) {
-        const int64_t tile = u / C;
-        const int c = (int)(u - tile * C);
-        tk = (int)(tile / TM);
-        tm = (int)(tile % TM);
-        j = c / NB;
-        n = c - j * NB;
-    }
-    __device__ __forceinline__ void next_matrix(int C, int NB, int64_t TM) {
-        n = 0;
-        if (++j * NB < C) return;
-        j = 0;
-        if (++tm < TM) return;
-        tm = 0;
-        ++tk;
-    }
-};
-
 // Bytes j of two rows' words as a pair of bf16 values.
 __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j) {
     const uint32_t t = __byte_perm(wa, wb, (uint32_t)(j | (j << 4) | ((4 + j) << 8) | ((4 + j) << 12)));
@@ -108,7 +87,8 @@ __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j
 template <int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8X_WARPS * 32, 1)
 k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
-        const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p) {
+        const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p,
+        I8Plan plan) {
     using Cfg = I8DxCfg<NT>;
     constexpr int S = Cfg::S, R = Cfg::R, U = Cfg::U;
     static_assert(R >= S && S >= I8X_GROUPS, "the converters' parity waits");
@@ -119,9 +99,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     const uint32_t rank = cluster_rank();
 
     const int NB = (p.N + U * I8X_NC - 1) / (U * I8X_NC), C = NB * p.nw;
-    const int64_t TK = (p.K + 255) / 256, TM = (p.M + NT - 1) / NT;
-    const int64_t units = TK * TM * C, G = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    const int64_t u0 = i8_run_start(pair, units, G), u1 = i8_run_start(pair + 1, units, G);
+    const int64_t TM = (p.M + NT - 1) / NT;
+    const int pair = blockIdx.x >> 1, n_segs = i8_segs(plan, pair);
 
     if (tid == 0) {
         for (int s = 0; s < R; ++s) {
@@ -159,61 +138,55 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 
     if (warp == 0) {
         const bool issuer = elect_one();
-        I8DxPlace at(u0, C, NB, TM);
         int r = 0;
         uint32_t ph = 1;
         bool ok = true;
-        int64_t left = u1 - u0;
-        while (left > 0 && ok) {   // along the channels of one matrix
-            const int n = (int)min(left, (int64_t)(NB - at.n));
-            const CUtensorMap* map = at.j ? &wmap1 : &wmap0;
-            const int k0 = at.tk * 256 + (int)rank * 128;
-            int n0 = at.n * U * I8X_NC;
-            for (int i = 0; i < n; ++i, n0 += U * I8X_NC) {
+        for (int j = 0; j < n_segs && ok; ++j) {
+            const I8Seg g = i8_seg(plan, pair, j, C);
+            const int k0 = (int)(g.tile / TM) * 256 + (int)rank * 128;
+            for (int c = g.k0; c < g.k1; ++c) {
+                const bool second = c >= NB;   // the second matrix's channels
                 ok = i8_wait_warp(&sm.raw_empty[r], ph);
                 if (!ok) break;
                 if (issuer) {
                     mbar_arrive_expect_tx(&sm.raw_full[r], U * I8X_RAW);
-                    if (!kI8WaitTest) i8_tma_load<false>(sm.raw[r], map, k0, n0, smem_u32(&sm.raw_full[r]));
+                    if (!kI8WaitTest)
+                        i8_tma_load<false>(sm.raw[r], second ? &wmap1 : &wmap0, k0, (second ? c - NB : c) * U * I8X_NC,
+                                           smem_u32(&sm.raw_full[r]));
                 }
                 ++armed;
                 if (kI8WaitTest) break;   // armed, no copy
                 if (++r == R) { r = 0; ph ^= 1u; }
             }
             if (kI8WaitTest) break;
-            left -= n;
-            at.next_matrix(C, NB, TM);
         }
         if (!ok && issuer) timed_out();
         __syncwarp();
     } else if (warp == I8X_WARPS - 1) {
         const bool issuer = elect_one();
-        I8DxPlace at(u0, C, NB, TM);
         const uint32_t full0 = cluster_addr(&sm.full[0], 0);
         int s = 0;
         uint32_t ph = 1;
         bool ok = !kI8WaitTest;
-        int64_t left = u1 - u0;
-        while (left > 0 && ok) {
-            const int n = (int)min(left, (int64_t)(NB - at.n));
-            const CUtensorMap* map = at.j ? &gmap1 : &gmap0;
-            const int m0 = at.tm * NT + (int)rank * (NT / 2);
-            int n0 = at.n * U * I8X_NC;
-            for (int i = 0; i < n; ++i, n0 += U * I8X_NC) {
+        for (int j = 0; j < n_segs && ok; ++j) {
+            const I8Seg g = i8_seg(plan, pair, j, C);
+            const int m0 = (int)(g.tile % TM) * NT + (int)rank * (NT / 2);
+            for (int c = g.k0; c < g.k1; ++c) {
+                const bool second = c >= NB;
                 ok = i8_wait_warp(&sm.empty[s], ph);
                 if (!ok) break;
                 if (issuer) {
                     // the first CTA's barrier counts both CTAs' bytes
                     if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * U * Cfg::B);
+                    const int n0 = (second ? c - NB : c) * U * I8X_NC;
 #pragma unroll
                     for (int b = 0; b < U; ++b)
-                        i8_tma_load<true>(sm.b[s] + b * Cfg::B_STRIDE, map, n0 + b * I8X_NC, m0, full0 + 8u * (uint32_t)s);
+                        i8_tma_load<true>(sm.b[s] + b * Cfg::B_STRIDE, second ? &gmap1 : &gmap0, n0 + b * I8X_NC, m0,
+                                          full0 + 8u * (uint32_t)s);
                 }
                 ++armed;
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
-            left -= n;
-            at.next_matrix(C, NB, TM);
         }
         // the releases of the last stages arrive before the CTA ends
         for (int i = max(0, armed - S); ok && i < armed; ++i)
@@ -226,11 +199,10 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             const bool issuer = elect_one();
             int s = 0, seg = 0;
             uint32_t ph = 0;
-            int64_t next = (u0 / C + 1) * C;
             bool ok = true;
-            for (int64_t u = u0; u < u1 && ok; next += C) {
-                const int n = (int)(min(u1, next) - u);
-                const int buf = seg & 1;
+            for (int j = 0; j < n_segs && ok; ++j) {
+                const I8Seg g = i8_seg(plan, pair, j, C);
+                const int n = g.k1 - g.k0, buf = seg & 1;
                 ok = i8_wait_warp<true>(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u);
                 if (!ok) break;
                 i8_fence_after();
@@ -250,7 +222,6 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
                 if (ok) ++seg;
-                u += n;
             }
             // the peer's last arrivals land before this CTA ends
             for (int i = max(0, seg - 2); ok && i < seg; ++i)
@@ -261,10 +232,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     } else if (warp < 2 + I8X_EPI) {
         const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 64
         const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
-            const int64_t tile = u / C, t0 = tile * C, t1 = t0 + C;
-            const int64_t end = min(u1, t1);
+        for (int seg = 0; seg < n_segs; ++seg) {
+            const I8Seg g = i8_seg(plan, pair, seg, C);
             const int buf = seg & 1;
             bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
@@ -273,16 +242,13 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 break;
             }
             i8_fence_after();
-            const int64_t k = (tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (tile % TM) * NT;
+            const int64_t k = (g.tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (g.tile % TM) * NT;
             const int mc = (int)min((int64_t)NT, p.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NT);
-            const int64_t c0 = i8_run_of(t0, units, G), c1 = i8_run_of(t1 - 1, units, G);
-            auto slot_of = [&](int64_t c) {
-                return p.slots + (((c * 2 + (c == c0 ? 1 : 0)) * 2 + rank) * NT) * 128 + quad * 32 + lane;
-            };
-            // A cut tile: when all others have arrived already (the usual case
-            // for the run that holds the tile's start, its last work), this
-            // one only adds; else it leaves its part and counts itself in.
+            const int c0 = g.c0, c1 = g.c1;
+            auto slot_of = [&](int c) { return p.slots + ((size_t)(c * 2 + rank) * NT) * 128 + quad * 32 + lane; };
+            // A cut tile: when all others have arrived already, this one only
+            // adds; else it leaves its part and counts itself in.
             uint32_t* counter = p.counters + (c0 * 2 + rank) * I8X_EPI + warp - 2;
             const uint32_t others = (uint32_t)(c1 - c0);
             bool mine = 32 * half < mc;
@@ -314,7 +280,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    for (int64_t o = c0; o <= c1; ++o) {   // in the order of the runs
+                    for (int o = c0; o <= c1; ++o) {   // in the order of the pieces
                         uint32_t t[32];
                         if (o == pair) {
                             i8_tmem_ld32(taddr + (uint32_t)c, t);
@@ -346,7 +312,6 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             i8_fence_before();
             __syncwarp();
             if (lane == 0) cluster_arrive(empty_bar + 8u * (uint32_t)buf);
-            u = end;
         }
     } else {
         // converters: a group takes every other stage, so that two stages'
@@ -362,7 +327,11 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             at[j] = (row >> 3) * 1024 + (row & 7) * 128 + (((uint32_t)c ^ (row & 7)) << 4);
         }
         const uint32_t full0 = cluster_addr(&sm.full[0], 0);
-        const uint32_t n_units = (uint32_t)(u1 - u0);   // a CTA's run: far below 2^32
+        uint32_t n_units = (uint32_t)plan.full * (uint32_t)C;   // stages in all: far below 2^32
+        if (n_segs > plan.full) {
+            const I8Seg g = i8_seg(plan, pair, plan.full, C);
+            n_units += (uint32_t)(g.k1 - g.k0);
+        }
         // stage and phase of this group's unit in either ring
         uint32_t r = group, s = group, rph = 0, sph = 1;
         for (uint32_t it = group; it < n_units; it += I8X_GROUPS) {

@@ -5,29 +5,30 @@
 //   D[n][m] = sum_k w[n][k] x[m][k]    (128 channels x NT tokens, s32 in TMEM)
 //
 // The channels take the 128 lanes (the wide side of the instruction) and the
-// tokens its columns, so one token costs no more tensor work than NT.  The
-// work is the list of (128-channel tile, 128-byte chunk of k) units, cut into
-// equal contiguous runs, one a CTA and one CTA an SM, whatever the shape: no
-// wave is left half empty and every SM has the same bytes to fetch.  A CTA
-// keeps its whole shared memory in flight as TMA copies.
-// A tile that is cut gets its partial sums through global memory: every
-// contributor writes its own slot, and the last to arrive adds them.  The
-// sums are integers, so the result does not depend on the cuts or the order.
+// tokens its columns, so one token costs no more tensor work than NT.  A CTA
+// keeps its whole shared memory in flight as TMA copies, one CTA an SM.
+//
+// Work: every CTA takes whole tiles, a round of them at a time; the tiles of
+// the last, partial round are cut along k into equal pieces, one a CTA, when
+// there are at least two CTAs for each (I8Plan).  A cut costs its tile a round
+// trip through global memory: every contributor writes its own slot and the
+// last to arrive adds them -- integers, so the result depends neither on the
+// cuts nor on the order.  Where a round has more tiles than half the SMs it is
+// left whole: half of them still draw nearly all of HBM's bandwidth (gate and
+// up 14336 x 4096, 112 tiles: 64 tokens 36 us cut into equal shares, 24 whole).
 // Gated: gate and up tiles ride in the same stage, against the same tokens.
 //
-// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-9 read the
-// accumulators (two for each TMEM lane quadrant, taking alternate groups of 16
-// tokens).  Every wait is bounded.
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the
+// accumulators (four for each TMEM lane quadrant, each taking every fourth group
+// of eight tokens: a group costs mostly latency).  Every wait is bounded.
 #pragma once
-#include <type_traits>
-
 #include "i8_gate.cuh"
 #include "i8_tc.cuh"
 #include "k_i8_rows.cuh"
 
 namespace mpq {
 
-constexpr int I8S_EPI = 8;                            // two for each TMEM lane quadrant
+constexpr int I8S_EPI = 16;                           // four for each TMEM lane quadrant
 constexpr int I8S_WARPS = 2 + I8S_EPI;
 constexpr int I8S_MAX_CTAS = 256;                     // counters in the workspace
 constexpr int I8_KC = 128;                            // bytes of k in a stage
@@ -69,20 +70,42 @@ struct I8Product {
     int32_t* slots;      // partial sums
 };
 
+// What a sum (or a pair of sums) becomes.  MODE 0: the product, 1: the gated
+// product, 2: the gradients of gate and up, plain (v) and scaled (g).
+struct I8Value {
+    float v, v1, g, g1;
+};
+template <int MODE, int ACT>
+__device__ __forceinline__ I8Value i8_value(int acc0, int acc1, float ws0, float ws1, float xs, float dh) {
+    I8Value o{};
+    o.v = ((float)acc0 * ws0) * xs;
+    if (MODE > 0) {
+        const float b = ((float)acc1 * ws1) * xs;
+        const Gate gt = gate_eval<ACT>(o.v);
+        if (MODE == 1) {
+            o.v = gt.act * b;
+        } else {
+            o.v = dh * b * gt.grad;
+            o.v1 = dh * gt.act;
+            o.g = o.v * ws0;
+            o.g1 = o.v1 * ws1;
+        }
+    }
+    return o;
+}
+
 // A column of outputs: channel n of tokens m, m + 1, ..., with the addresses
 // counted along (64-bit products for every element cost more than its
-// arithmetic).  MODE 0: linear, 1: gated, 2: the gradients of gate and up.
-template <int MODE, int ACT>
+// arithmetic).
+template <int MODE>
 struct I8Column {
     uint8_t* y;
     const uint16_t* dh;
     uint16_t *d0, *d1, *g;
     int64_t ystep, dhstep, dstep, gstep, up_off;
-    float ws0, ws1;
     bool bf16;
 
-    __device__ __forceinline__ I8Column(const I8Product& p, int64_t m, int64_t n, float ws0_, float ws1_)
-        : ws0(ws0_), ws1(ws1_) {
+    __device__ __forceinline__ I8Column(const I8Product& p, int64_t m, int64_t n) {
         if (MODE < 2) {
             bf16 = p.y_bf16 != 0;
             ystep = p.ldy * (bf16 ? 2 : 4);
@@ -98,50 +121,77 @@ struct I8Column {
             up_off = p.up_off;
         }
     }
-    __device__ __forceinline__ float load_dh() const { return MODE == 2 ? I8Elem<true>::get(*dh) : 0.f; }
-    __device__ __forceinline__ void next_dh() { if (MODE == 2) dh += dhstep; }
-    __device__ __forceinline__ void next() {
-        if (MODE < 2) {
-            y += ystep;
-        } else {
-            if (d0) { d0 += dstep; d1 += dstep; }
-            g += gstep;
-        }
+    __device__ __forceinline__ float next_dh() {
+        const float v = I8Elem<true>::get(*dh);
+        dh += dhstep;
+        return v;
     }
-    __device__ __forceinline__ void put(int acc0, int acc1, float xs, float dhv) const {
-        const float a = ((float)acc0 * ws0) * xs;
-        float v = a;
-        if (MODE > 0) {
-            const float b = ((float)acc1 * ws1) * xs;
-            const Gate gt = gate_eval<ACT>(a);
-            if (MODE == 2) {
-                const float dg = dhv * b * gt.grad, du = dhv * gt.act;
-                if (d0) {
-                    *d0 = (uint16_t)pack_bf16(dg, 0.f);
-                    *d1 = (uint16_t)pack_bf16(du, 0.f);
-                }
-                g[0] = (uint16_t)pack_bf16(dg * ws0, 0.f);
-                g[up_off] = (uint16_t)pack_bf16(du * ws1, 0.f);
-                return;
+    // The first `left` of N values.  Values are computed before, without a
+    // branch between them, so that their latencies overlap.
+    template <int N>
+    __device__ __forceinline__ void put(const I8Value (&o)[N], int left) {
+        if (MODE < 2) {
+            if (bf16) {
+#pragma unroll
+                for (int i = 0; i < N; ++i, y += ystep)
+                    if (i < left) *reinterpret_cast<uint16_t*>(y) = (uint16_t)pack_bf16(o[i].v, 0.f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i, y += ystep)
+                    if (i < left) *reinterpret_cast<float*>(y) = o[i].v;
             }
-            v = gt.act * b;
+            return;
         }
-        if (bf16) *reinterpret_cast<uint16_t*>(y) = (uint16_t)pack_bf16(v, 0.f);
-        else *reinterpret_cast<float*>(y) = v;
+        if (d0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i, d0 += dstep, d1 += dstep)
+                if (i < left) {
+                    *d0 = (uint16_t)pack_bf16(o[i].v, 0.f);
+                    *d1 = (uint16_t)pack_bf16(o[i].v1, 0.f);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i, g += gstep)
+            if (i < left) {
+                g[0] = (uint16_t)pack_bf16(o[i].g, 0.f);
+                g[up_off] = (uint16_t)pack_bf16(o[i].g1, 0.f);
+            }
     }
 };
 
-// Unit u belongs to CTA u * G / units (rounded down the same way as the
-// runs' ends): run c is [c * units / G, (c + 1) * units / G).
-__device__ __forceinline__ int64_t i8_run_start(int64_t c, int64_t units, int64_t G) { return c * units / G; }
-__device__ __forceinline__ int64_t i8_run_of(int64_t u, int64_t units, int64_t G) {
-    return ((u + 1) * G - 1) / units;
+// The work of G workers (CTAs or pairs): `full` rounds of whole tiles, then
+// pieces of the `rem` tiles left, `cuts` a tile.
+struct I8Plan {
+    int full, rem, cuts, workers;
+};
+// Segment j of worker w: a tile and its chunks [k0, k1); contributors c0 .. c1.
+struct I8Seg {
+    int64_t tile;
+    int k0, k1, c0, c1;
+};
+__device__ __forceinline__ int i8_segs(const I8Plan& p, int w) { return p.full + (w < p.rem * p.cuts ? 1 : 0); }
+__device__ __forceinline__ I8Seg i8_seg(const I8Plan& p, int w, int j, int chunks) {
+    I8Seg s;
+    if (j < p.full) {
+        s.tile = (int64_t)j * p.workers + w;
+        s.k0 = 0;
+        s.k1 = chunks;
+        s.c0 = s.c1 = w;
+        return s;
+    }
+    const int t = w / p.cuts, piece = w - t * p.cuts;
+    s.tile = (int64_t)p.full * p.workers + t;
+    s.k0 = (int)((int64_t)piece * chunks / p.cuts);
+    s.k1 = (int)((int64_t)(piece + 1) * chunks / p.cuts);
+    s.c0 = t * p.cuts;
+    s.c1 = s.c0 + p.cuts - 1;
+    return s;
 }
 
 template <int NT, int MODE, int ACT>
 __global__ void __launch_bounds__(I8S_WARPS * 32, 1)
 k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap0,
-            const __grid_constant__ CUtensorMap wmap1, I8Product p) {
+            const __grid_constant__ CUtensorMap wmap1, I8Product p, I8Plan plan) {
     constexpr int NW = MODE == 0 ? 1 : 2;
     using Cfg = I8StreamCfg<NT, NW>;
     constexpr int S = Cfg::STAGES, BUFS = Cfg::BUFS;
@@ -151,9 +201,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const int KB = (p.K + I8_KC - 1) / I8_KC;
-    const int T = (p.N + 127) / 128, TM = (p.M + NT - 1) / NT;
-    const int64_t units = (int64_t)TM * T * KB, G = gridDim.x, cta = blockIdx.x;
-    const int64_t u0 = i8_run_start(cta, units, G), u1 = i8_run_start(cta + 1, units, G);
+    const int T = (p.N + 127) / 128, cta = blockIdx.x, n_segs = i8_segs(plan, cta);
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -183,34 +231,34 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         set_error(p.err, MPQ_ERR_TIMEOUT);
         sm.abort_flag = 1;
     };
-    int armed = 0, segs = 0;
+    int armed = 0;
 
     if (warp == 0) {
         const bool issuer = elect_one();
-        const int64_t tile = u0 / KB;
-        int kb = (int)(u0 - tile * KB), t = (int)(tile % T), mt = (int)(tile / T), s = 0;
+        int s = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (int64_t u = u0; u < u1; ++u) {
-            ok = i8_wait_warp(&sm.empty[s], ph);
-            if (!ok) break;
-            ++armed;
-            if (issuer) {
-                mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
-                if (!kI8WaitTest) {
-                    const uint32_t bar = smem_u32(&sm.full[s]);
-                    const int kc = kb * I8_KC;
-                    i8_tma_load<false>(sm.st[s], &wmap0, kc, t * 128, bar);
-                    if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, t * 128, bar);
-                    i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, mt * NT, bar);
+        for (int j = 0; j < n_segs && ok; ++j) {
+            const I8Seg g = i8_seg(plan, cta, j, KB);
+            const int n0 = (int)(g.tile % T) * 128, m0 = (int)(g.tile / T) * NT;
+            for (int kb = g.k0; kb < g.k1; ++kb) {
+                ok = i8_wait_warp(&sm.empty[s], ph);
+                if (!ok) break;
+                ++armed;
+                if (issuer) {
+                    mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
+                    if (!kI8WaitTest) {
+                        const uint32_t bar = smem_u32(&sm.full[s]);
+                        const int kc = kb * I8_KC;
+                        i8_tma_load<false>(sm.st[s], &wmap0, kc, n0, bar);
+                        if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, n0, bar);
+                        i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, m0, bar);
+                    }
                 }
+                if (kI8WaitTest) break;   // armed, no copy
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (kI8WaitTest) break;   // armed, no copy
-            if (++s == S) { s = 0; ph ^= 1u; }
-            if (++kb == KB) {   // the next tile
-                kb = 0;
-                if (++t == T) { t = 0; ++mt; }
-            }
+            if (kI8WaitTest) break;
         }
         if (!ok && issuer) timed_out();
         __syncwarp();
@@ -219,12 +267,11 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         const bool issuer = elect_one();
         int s = 0;
         uint32_t ph = 0;
-        int64_t next = (u0 / KB + 1) * KB;
         bool ok = true;
-        for (int64_t u = u0; u < u1 && ok; next += KB) {
-            const int n = (int)(min(u1, next) - u);
-            const int buf = segs % BUFS;
-            ok = i8_wait_warp(&sm.d_empty[buf], ((uint32_t)(segs / BUFS) & 1u) ^ 1u);
+        for (int j = 0; j < n_segs && ok; ++j) {
+            const I8Seg g = i8_seg(plan, cta, j, KB);
+            const int n = g.k1 - g.k0, buf = j % BUFS;
+            ok = i8_wait_warp(&sm.d_empty[buf], ((uint32_t)(j / BUFS) & 1u) ^ 1u);
             if (!ok) break;
             i8_fence_after();
             for (int i = 0; i < n; ++i) {
@@ -242,19 +289,15 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 }
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (ok) ++segs;
-            u += n;
         }
         if (!ok && issuer) timed_out();
         __syncwarp();
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
-            const int64_t tile = u / KB, t0 = tile * KB, t1 = t0 + KB;
-            const int64_t end = min(u1, t1);
+        const int quad = warp & 3, part = (warp - 2) >> 2;
+        for (int seg = 0; seg < n_segs; ++seg) {
+            const I8Seg g = i8_seg(plan, cta, seg, KB);
             const int buf = seg % BUFS;
-            const int n = (int)(tile % T) * 128 + quad * 32 + lane, m0 = (int)(tile / T) * NT;
+            const int n = (int)(g.tile % T) * 128 + quad * 32 + lane, m0 = (int)(g.tile / T) * NT;
             const int mc = min(NT, p.M - m0);
             const bool in = n < p.N;
             const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
@@ -266,32 +309,28 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             }
             i8_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NW * NT);
-            // contributors c0 .. c1; this CTA's slot: 1 for the tile that
-            // starts inside its run, 0 for the one that began before it
-            const int64_t c0 = i8_run_of(t0, units, G), c1 = i8_run_of(t1 - 1, units, G);
-            auto slot_of = [&](int64_t c) {
-                return p.slots + ((c * 2 + (c == c0 ? 1 : 0)) * NW * NT) * 128 + quad * 32 + lane;
-            };
+            const int c0 = g.c0, c1 = g.c1;
+            auto slot_of = [&](int c) { return p.slots + (size_t)c * (NW * NT * 128) + quad * 32 + lane; };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
             uint32_t* counter = p.counters + c0 * I8S_EPI + warp - 2;
             const uint32_t others = (uint32_t)(c1 - c0);
-            bool mine = 16 * half < mc;   // this warp writes the results
+            bool mine = 8 * part < mc;   // this warp writes the results
             if (mine && c0 != c1) {
                 uint32_t seen = 0;
                 if (lane == 0) seen = i8_load_acquire(counter);
                 if (__shfl_sync(0xffffffffu, seen, 0) != others) {
                     int32_t* slot = slot_of(cta);
-                    for (int c = 16 * half; c < mc; c += 32) {
+                    for (int c = 8 * part; c < mc; c += 32) {
+                        uint32_t r[NW][8];
 #pragma unroll
-                        for (int j = 0; j < NW; ++j) {
-                            uint32_t r[16];
-                            i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
-                            i8_tmem_wait();
+                        for (int j = 0; j < NW; ++j) i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r[j]);
+                        i8_tmem_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[i];
-                        }
+                        for (int j = 0; j < NW; ++j)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[j][i];
                     }
                     __threadfence();
                     __syncwarp();
@@ -303,70 +342,54 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     __threadfence();
                 }
             }
-            // Columns c .. c + CW - 1: the sums, then the outputs.  Loads come
+            // Eight columns at a time: the sums, then the outputs.  Loads come
             // first (a store may alias them for all the compiler knows, and
-            // each would wait for the one before), Q contributors' at a time.
-            auto finish = [&](auto cw, auto qn, int c) {
-                constexpr int CW = decltype(cw)::value, Q = decltype(qn)::value;
+            // each would wait for the one before), two contributors' together.
+            for (int c = 8 * part; mine && c < mc; c += 32) {
                 const int left = mc - c;
-                float xs[CW], dh[MODE == 2 ? CW : 1];
+                float xs[8], dh[MODE == 2 ? 8 : 1];
 #pragma unroll
-                for (int i = 0; i < CW; ++i) xs[i] = i < left ? p.xs[m0 + c + i] : 0.f;
-                I8Column<MODE, ACT> col(p, m0 + c, in ? n : 0, ws0, ws1);
+                for (int i = 0; i < 8; ++i) xs[i] = i < left ? p.xs[m0 + c + i] : 0.f;
+                I8Column<MODE> col(p, m0 + c, in ? n : 0);
                 if (MODE == 2)
 #pragma unroll
-                    for (int i = 0; i < CW; ++i)
-                        if (i < left) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
-                int acc[NW][CW];
-#pragma unroll
-                for (int j = 0; j < NW; ++j) {
-                    uint32_t r[CW];
-                    if (CW == 16) i8_tmem_ld16(taddr + (uint32_t)(j * NT + c), r);
-                    else i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r);
-                    i8_tmem_wait();
-#pragma unroll
-                    for (int i = 0; i < CW; ++i) acc[j][i] = (int)r[i];
-                }
+                    for (int i = 0; i < 8; ++i) dh[MODE == 2 ? i : 0] = i < left ? col.next_dh() : 0.f;
+                int acc[NW][8] = {};
                 if (c0 != c1)
-                    for (int64_t o = c0; o <= c1; o += Q) {
-                        int t[Q][NW][CW];
+                    for (int o = c0; o <= c1; o += 2) {
+                        int t[2][NW][8];
 #pragma unroll
-                        for (int q = 0; q < Q; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             const bool add = o + q <= c1 && o + q != cta;
                             const int32_t* slot = slot_of(o + q);
 #pragma unroll
                             for (int j = 0; j < NW; ++j)
 #pragma unroll
-                                for (int i = 0; i < CW; ++i)
+                                for (int i = 0; i < 8; ++i)
                                     t[q][j][i] = add && i < left ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
                         }
 #pragma unroll
-                        for (int q = 0; q < Q; ++q)
+                        for (int q = 0; q < 2; ++q)
 #pragma unroll
                             for (int j = 0; j < NW; ++j)
 #pragma unroll
-                                for (int i = 0; i < CW; ++i) acc[j][i] += t[q][j][i];
+                                for (int i = 0; i < 8; ++i) acc[j][i] += t[q][j][i];
                     }
-                if (in) {
+                uint32_t r[NW][8];
 #pragma unroll
-                    for (int i = 0; i < CW; ++i)
-                        if (i < left) {
-                            col.put(acc[0][i], acc[NW - 1][i], xs[i], dh[MODE == 2 ? i : 0]);
-                            col.next();
-                        }
-                }
+                for (int j = 0; j < NW; ++j) i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r[j]);
+                i8_tmem_wait();
+                I8Value o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = i8_value<MODE, ACT>(acc[0][i] + (int)r[0][i], acc[NW - 1][i] + (int)r[NW - 1][i], ws0, ws1,
+                                               xs[i], dh[MODE == 2 ? i : 0]);
+                if (in) col.put(o, left);
                 __syncwarp();
-            };
-            if (mine) {
-                if (mc <= 8) finish(std::integral_constant<int, 8>{}, std::integral_constant<int, 4 / NW>{}, 0);
-                else
-                    for (int c = 16 * half; c < mc; c += 32)
-                        finish(std::integral_constant<int, 16>{}, std::integral_constant<int, 2 / NW>{}, c);
             }
             i8_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.d_empty[buf]);
-            u = end;
         }
     }
     // copies and MMAs in flight land before shared memory and TMEM are given

@@ -196,24 +196,23 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
                 const int64_t n = n0 + c + lane;
                 const bool in = n < p.N;
                 const float ws0 = in ? p.ws[0][n] : 0.f, ws1 = NW == 2 && in ? p.ws[1][n] : 0.f;
-                I8Column<MODE, ACT> col(p, m0, n, ws0, ws1);
+                I8Column<MODE> col(p, m0, in ? n : 0);
                 for (int i0 = 0; i0 < rows; i0 += 8) {
+                    const int left = rows - i0;
                     float dh[MODE == 2 ? 8 : 1];
                     if (MODE == 2)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (in && i0 + i < rows) { dh[MODE == 2 ? i : 0] = col.load_dh(); col.next_dh(); }
+                        for (int i = 0; i < 8; ++i) dh[MODE == 2 ? i : 0] = i < left ? col.next_dh() : 0.f;
+                    I8Value o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = i0 + i;
                         const int a0 = __float_as_int(pa[r * 32 + (lane ^ r)]);
                         const int a1 = NW == 2 ? __float_as_int(pb[r * 32 + (lane ^ r)]) : 0;
-                        const float s = __shfl_sync(0xffffffffu, xs, r);
-                        if (in && r < rows) {
-                            col.put(a0, a1, s, dh[MODE == 2 ? i : 0]);
-                            col.next();
-                        }
+                        o[i] = i8_value<MODE, ACT>(a0, a1, ws0, ws1, __shfl_sync(0xffffffffu, xs, r),
+                                                   dh[MODE == 2 ? i : 0]);
                     }
+                    if (in) col.put(o, left);
                 }
                 __syncwarp();
             }

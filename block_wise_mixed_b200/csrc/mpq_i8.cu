@@ -165,8 +165,8 @@ constexpr int kStreamMaxM = MAXM;
 // that a call writes before it reads.  The zeroed part has one size for all
 // mpq_i8_* calls, so one workspace serves them all, one after another.
 constexpr size_t kErrBytes = 256;
-constexpr size_t kI8ZeroBytes = kErrBytes + 5120;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
-static_assert(kSMs * I8S_EPI * 4 <= 5120 && kPairs * 2 * I8X_EPI * 4 <= 5120, "counters");
+constexpr size_t kI8ZeroBytes = kErrBytes + 9728;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
+static_assert(kSMs * I8S_EPI * 4 <= 9728 && kPairs * 2 * I8X_EPI * 4 <= 9728 && kI8ZeroBytes % 256 == 0, "counters");
 
 inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
@@ -184,31 +184,39 @@ inline int dx_nt(int64_t M) { return FORCE_DX; }
 inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 #endif
-#ifndef CUTK
-#define CUTK 14.0
-#endif
-// Runs that a tile of `chunks` units may be cut into: a unit costs about as
-// long (0.35 us at an SM's share of HBM) as the last contributor takes to add
-// 14 columns of one more partial sum, so n runs cost chunks / n + n cols / 14
-// units, least at n = sqrt(14 chunks / cols).
+// Pieces that a tile of `chunks` stages may be cut into: a stage costs about as
+// long as the last contributor takes to add 14 columns of one more partial sum,
+// so n pieces cost chunks / n + n cols / 14, least at n = sqrt(14 chunks / cols).
 inline int64_t max_cuts(int64_t chunks, int64_t cols) {
-    return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(CUTK * (double)chunks / (double)cols)));
+    return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(14.0 * (double)chunks / (double)cols)));
 }
-inline int64_t stream_ctas(int64_t M, int64_t N, int64_t K, int nw) {
-    const int64_t chunks = div_up(K, I8_KC), tiles = div_up(M, stream_nt(M)) * div_up(N, 128);
-    return std::min<int64_t>({(int64_t)kSMs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, stream_nt(M)) * nw)});
+I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers) {
+    I8Plan p{};
+    p.full = (int)(tiles / workers);
+    p.rem = (int)(tiles % workers);
+    p.cuts = 1;
+    if (p.rem) p.cuts = (int)std::min<int64_t>({workers / p.rem, chunks, max_cuts(chunks, cols)});
+    p.workers = p.full ? workers : p.rem * p.cuts;
+    return p;
 }
-inline int64_t dx_pairs(int64_t M, int64_t N, int64_t K, int nw) {
-    const int64_t chunks = div_up(N, I8X_NC * (dx_nt(M) == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U)) * nw, tiles = div_up(M, dx_nt(M)) * div_up(K, 256);
-    return std::min<int64_t>({(int64_t)kPairs, tiles * chunks, tiles * max_cuts(chunks, std::min<int64_t>(M, dx_nt(M)))});
+inline I8Plan stream_plan(int64_t M, int64_t N, int64_t K, int nw) {
+    const int nt = stream_nt(M);
+    return make_plan(div_up(M, nt) * div_up(N, 128), div_up(K, I8_KC), std::min<int64_t>(M, nt) * nw, kSMs);
+}
+inline I8Plan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
+    const int nt = dx_nt(M), u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
+    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs);
 }
 
-// Partial sums: two slots a CTA (or pair), 128 lanes x NT columns each.
+// Partial sums: a slot a worker with a piece of a cut tile, 128 lanes x NT columns.
 inline size_t product_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    return M > kStreamMaxM ? 0 : (size_t)stream_ctas(M, N, K, nw) * 2 * nw * stream_nt(M) * 128 * 4;
+    if (M > kStreamMaxM) return 0;
+    const I8Plan p = stream_plan(M, N, K, nw);
+    return p.cuts < 2 ? 0 : (size_t)p.rem * p.cuts * nw * stream_nt(M) * 128 * 4;
 }
 inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    return (size_t)dx_pairs(M, N, K, nw) * 2 * 2 * dx_nt(M) * 128 * 4;
+    const I8Plan p = dx_plan(M, N, K, nw);
+    return p.cuts < 2 ? 0 : (size_t)p.rem * p.cuts * 2 * dx_nt(M) * 128 * 4;
 }
 
 inline int64_t grad_ld(int64_t n) { return div_up(n, 64) * 64; }
@@ -309,8 +317,9 @@ mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& 
     CUtensorMap xm, w0, w1;
     if (!make_map(&xm, x, NT, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
         return MPQ_ERR_CUDA;
-    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)stream_ctas(p.M, p.N, p.K, NW)), I8S_WARPS * 32,
-                                                  sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p);
+    const I8Plan plan = stream_plan(p.M, p.N, p.K, NW);
+    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)plan.workers), I8S_WARPS * 32,
+                                                  sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p, plan);
 }
 
 template <int MODE, int ACT>
@@ -352,8 +361,9 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
         !make_map(&g0, g, true, p.M, p.N, ldg * 2, NT / 2, true) ||
         !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
-    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * dx_pairs(p.M, p.N, p.K, nw))), I8X_WARPS * 32,
-                                   sizeof(I8DxSmem<NT>) + 1024, stream, w0, w1, g0, g1, p);
+    const I8Plan plan = dx_plan(p.M, p.N, p.K, nw);
+    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * plan.workers)), I8X_WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
+                                   stream, w0, w1, g0, g1, p, plan);
 }
 
 mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, int64_t M,
