@@ -100,7 +100,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 
     const int NB = (p.N + U * I8X_NC - 1) / (U * I8X_NC), C = NB * p.nw;
     const int64_t TM = (p.M + NT - 1) / NT;
-    const int pair = blockIdx.x >> 1, n_segs = i8_segs(plan, pair);
+    const int pair = blockIdx.x >> 1;
+    const I8Work work(plan, pair, C);
+    const int n_segs = work.segs;
 
     if (tid == 0) {
         for (int s = 0; s < R; ++s) {
@@ -142,7 +144,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         uint32_t ph = 1;
         bool ok = true;
         for (int j = 0; j < n_segs && ok; ++j) {
-            const I8Seg g = i8_seg(plan, pair, j, C);
+            const I8Seg g = work.seg(j);
             const int k0 = (int)(g.tile / TM) * 256 + (int)rank * 128;
             for (int c = g.k0; c < g.k1; ++c) {
                 const bool second = c >= NB;   // the second matrix's channels
@@ -169,7 +171,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         uint32_t ph = 1;
         bool ok = !kI8WaitTest;
         for (int j = 0; j < n_segs && ok; ++j) {
-            const I8Seg g = i8_seg(plan, pair, j, C);
+            const I8Seg g = work.seg(j);
             const int m0 = (int)(g.tile % TM) * NT + (int)rank * (NT / 2);
             for (int c = g.k0; c < g.k1; ++c) {
                 const bool second = c >= NB;
@@ -201,7 +203,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             uint32_t ph = 0;
             bool ok = true;
             for (int j = 0; j < n_segs && ok; ++j) {
-                const I8Seg g = i8_seg(plan, pair, j, C);
+                const I8Seg g = work.seg(j);
                 const int n = g.k1 - g.k0, buf = seg & 1;
                 ok = i8_wait_warp<true>(&sm.d_empty[buf], ((uint32_t)(seg >> 1) & 1u) ^ 1u);
                 if (!ok) break;
@@ -233,7 +235,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 64
         const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
         for (int seg = 0; seg < n_segs; ++seg) {
-            const I8Seg g = i8_seg(plan, pair, seg, C);
+            const I8Seg g = work.seg(seg);
             const int buf = seg & 1;
             bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
@@ -246,7 +248,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             const int mc = (int)min((int64_t)NT, p.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NT);
             const int c0 = g.c0, c1 = g.c1;
-            auto slot_of = [&](int c) { return p.slots + ((size_t)(c * 2 + rank) * NT) * 128 + quad * 32 + lane; };
+            auto slot_of = [&](int c) {
+                return p.slots + ((size_t)(work.slot(c, c0) * 2 + rank) * NT) * 128 + quad * 32 + lane;
+            };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
             uint32_t* counter = p.counters + (c0 * 2 + rank) * I8X_EPI + warp - 2;
@@ -328,8 +332,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         }
         const uint32_t full0 = cluster_addr(&sm.full[0], 0);
         uint32_t n_units = (uint32_t)plan.full * (uint32_t)C;   // stages in all: far below 2^32
-        if (n_segs > plan.full) {
-            const I8Seg g = i8_seg(plan, pair, plan.full, C);
+        for (int j = plan.full; j < n_segs; ++j) {
+            const I8Seg g = work.seg(j);
             n_units += (uint32_t)(g.k1 - g.k0);
         }
         // stage and phase of this group's unit in either ring

@@ -8,14 +8,16 @@
 // tokens its columns, so one token costs no more tensor work than NT.  A CTA
 // keeps its whole shared memory in flight as TMA copies, one CTA an SM.
 //
-// Work: every CTA takes whole tiles, a round of them at a time; the tiles of
-// the last, partial round are cut along k into equal pieces, one a CTA, when
-// there are at least two CTAs for each (I8Plan).  A cut costs its tile a round
-// trip through global memory: every contributor writes its own slot and the
-// last to arrive adds them -- integers, so the result depends neither on the
-// cuts nor on the order.  Where a round has more tiles than half the SMs it is
-// left whole: half of them still draw nearly all of HBM's bandwidth (gate and
-// up 14336 x 4096, 112 tiles: 64 tokens 36 us cut into equal shares, 24 whole).
+// Work (I8Plan): every CTA takes whole tiles, a round of them at a time.  The
+// tiles of the last, partial round are cut along k into equal pieces, one a
+// CTA, when there are at least two CTAs for each.  A cut costs its tile a
+// round trip through global memory: every contributor writes its own slot and
+// the last to arrive adds them -- integers, so the result depends neither on
+// the cuts nor on the order.  A last round with more tiles than that stays
+// whole, since half of the SMs still draw nearly all of HBM's bandwidth (gate
+// and up 14336 x 4096, 112 tiles: 64 tokens 36 us cut into equal shares, 25
+// whole), unless its idle time is worth more than the cuts; then its chunks
+// are dealt out in equal runs, and a run may cross from one tile to the next.
 // Gated: gate and up tiles ride in the same stage, against the same tokens.
 //
 // Roles: warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the
@@ -159,34 +161,68 @@ struct I8Column {
     }
 };
 
-// The work of G workers (CTAs or pairs): `full` rounds of whole tiles, then
-// pieces of the `rem` tiles left, `cuts` a tile.
+// The work of `workers` CTAs or pairs: `full` rounds of whole tiles, then the
+// `rem` tiles left, in `cuts` equal pieces each (worker w: piece w), or with
+// cuts = 0 as equal runs over all their chunks.
 struct I8Plan {
     int full, rem, cuts, workers;
 };
-// Segment j of worker w: a tile and its chunks [k0, k1); contributors c0 .. c1.
+// A worker's j-th segment: a tile, its chunks [k0, k1), and the contributors
+// c0 .. c1 to that tile.
 struct I8Seg {
     int64_t tile;
     int k0, k1, c0, c1;
 };
-__device__ __forceinline__ int i8_segs(const I8Plan& p, int w) { return p.full + (w < p.rem * p.cuts ? 1 : 0); }
-__device__ __forceinline__ I8Seg i8_seg(const I8Plan& p, int w, int j, int chunks) {
-    I8Seg s;
-    if (j < p.full) {
-        s.tile = (int64_t)j * p.workers + w;
-        s.k0 = 0;
-        s.k1 = chunks;
-        s.c0 = s.c1 = w;
+struct I8Work {
+    const I8Plan& p;
+    int w, chunks, segs;
+    int64_t u0, u1;   // the run (cuts = 0)
+    __device__ __forceinline__ I8Work(const I8Plan& plan, int worker, int chunks_) : p(plan), w(worker), chunks(chunks_) {
+        segs = p.full;
+        u0 = u1 = 0;
+        if (p.cuts > 0) {
+            segs += w < p.rem * p.cuts ? 1 : 0;
+        } else {
+            const int64_t units = (int64_t)p.rem * chunks;
+            u0 = w * units / p.workers;
+            u1 = (w + 1) * units / p.workers;
+            if (u1 > u0) segs += (int)((u1 - 1) / chunks - u0 / chunks) + 1;
+        }
+    }
+    // the worker whose run holds unit u
+    __device__ __forceinline__ int run_of(int64_t u) const {
+        return (int)(((u + 1) * p.workers - 1) / ((int64_t)p.rem * chunks));
+    }
+    __device__ __forceinline__ I8Seg seg(int j) const {
+        I8Seg s;
+        if (j < p.full) {
+            s.tile = (int64_t)j * p.workers + w;
+            s.k0 = 0;
+            s.k1 = chunks;
+            s.c0 = s.c1 = w;
+            return s;
+        }
+        if (p.cuts > 0) {
+            const int t = w / p.cuts, piece = w - t * p.cuts;
+            s.tile = (int64_t)p.full * p.workers + t;
+            s.k0 = (int)((int64_t)piece * chunks / p.cuts);
+            s.k1 = (int)((int64_t)(piece + 1) * chunks / p.cuts);
+            s.c0 = t * p.cuts;
+            s.c1 = s.c0 + p.cuts - 1;
+            return s;
+        }
+        const int64_t t = u0 / chunks + (j - p.full), t0 = t * chunks;
+        s.tile = (int64_t)p.full * p.workers + t;
+        s.k0 = (int)(max(u0, t0) - t0);
+        s.k1 = (int)(min(u1, t0 + chunks) - t0);
+        s.c0 = run_of(t0);
+        s.c1 = run_of(t0 + chunks - 1);
         return s;
     }
-    const int t = w / p.cuts, piece = w - t * p.cuts;
-    s.tile = (int64_t)p.full * p.workers + t;
-    s.k0 = (int)((int64_t)piece * chunks / p.cuts);
-    s.k1 = (int)((int64_t)(piece + 1) * chunks / p.cuts);
-    s.c0 = t * p.cuts;
-    s.c1 = s.c0 + p.cuts - 1;
-    return s;
-}
+    // Worker c's slot for a tile with first contributor c0: a run has two, one
+    // for the tile it enters in the middle and one for the tile it starts.
+    __device__ __forceinline__ int slot(int c, int c0) const { return p.cuts > 0 ? c : 2 * c + (c == c0 ? 1 : 0); }
+};
 
 template <int NT, int MODE, int ACT>
 __global__ void __launch_bounds__(I8S_WARPS * 32, 1)
@@ -201,7 +237,9 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     const int KB = (p.K + I8_KC - 1) / I8_KC;
-    const int T = (p.N + 127) / 128, cta = blockIdx.x, n_segs = i8_segs(plan, cta);
+    const int T = (p.N + 127) / 128, cta = blockIdx.x;
+    const I8Work work(plan, cta, KB);
+    const int n_segs = work.segs;
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -239,7 +277,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         uint32_t ph = 1;
         bool ok = true;
         for (int j = 0; j < n_segs && ok; ++j) {
-            const I8Seg g = i8_seg(plan, cta, j, KB);
+            const I8Seg g = work.seg(j);
             const int n0 = (int)(g.tile % T) * 128, m0 = (int)(g.tile / T) * NT;
             for (int kb = g.k0; kb < g.k1; ++kb) {
                 ok = i8_wait_warp(&sm.empty[s], ph);
@@ -269,7 +307,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
         uint32_t ph = 0;
         bool ok = true;
         for (int j = 0; j < n_segs && ok; ++j) {
-            const I8Seg g = i8_seg(plan, cta, j, KB);
+            const I8Seg g = work.seg(j);
             const int n = g.k1 - g.k0, buf = j % BUFS;
             ok = i8_wait_warp(&sm.d_empty[buf], ((uint32_t)(j / BUFS) & 1u) ^ 1u);
             if (!ok) break;
@@ -295,7 +333,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     } else {
         const int quad = warp & 3, part = (warp - 2) >> 2;
         for (int seg = 0; seg < n_segs; ++seg) {
-            const I8Seg g = i8_seg(plan, cta, seg, KB);
+            const I8Seg g = work.seg(seg);
             const int buf = seg % BUFS;
             const int n = (int)(g.tile % T) * 128 + quad * 32 + lane, m0 = (int)(g.tile / T) * NT;
             const int mc = min(NT, p.M - m0);
@@ -310,7 +348,9 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             i8_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NW * NT);
             const int c0 = g.c0, c1 = g.c1;
-            auto slot_of = [&](int c) { return p.slots + (size_t)c * (NW * NT * 128) + quad * 32 + lane; };
+            auto slot_of = [&](int c) {
+                return p.slots + (size_t)work.slot(c, c0) * (NW * NT * 128) + quad * 32 + lane;
+            };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
             uint32_t* counter = p.counters + c0 * I8S_EPI + warp - 2;

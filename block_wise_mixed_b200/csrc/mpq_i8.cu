@@ -154,13 +154,6 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
 namespace {
 
 constexpr int kPairs = kSMs / 2;
-// Up to here the weights' bytes bound a product and k_i8_stream takes it;
-// above, k_i8_tile.
-#ifndef MAXM
-#define MAXM 128
-#endif
-constexpr int kStreamMaxM = MAXM;
-
 // Workspace: the error word, the counters (zero between calls), then scratch
 // that a call writes before it reads.  The zeroed part has one size for all
 // mpq_i8_* calls, so one workspace serves them all, one after another.
@@ -172,51 +165,84 @@ inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
 }
 
-// Tokens per tile of the streaming kernel, and of the gradient kernel.
-#ifdef FORCE_NT
-inline int stream_nt(int64_t M) { return FORCE_NT; }
-#else
-inline int stream_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-#endif
-#ifdef FORCE_DX
-inline int dx_nt(int64_t M) { return FORCE_DX; }
-#else
+// Tokens per tile of the gradient kernel.
 inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
-#endif
 // Pieces that a tile of `chunks` stages may be cut into: a stage costs about as
 // long as the last contributor takes to add 14 columns of one more partial sum,
 // so n pieces cost chunks / n + n cols / 14, least at n = sqrt(14 chunks / cols).
 inline int64_t max_cuts(int64_t chunks, int64_t cols) {
     return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(14.0 * (double)chunks / (double)cols)));
 }
-I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers) {
+// chunk_us: a stage's time.  Cuts, or equal runs, only where the time they take
+// off is worth more than a fix-up, about 5 us and 0.08 us a column (measured:
+// 16-token gradient of 8192 x 28672, 112 tiles on 74 pairs: 55 us in runs, 62
+// whole; one token through 14336 x 4096: 16.8 us in runs, 13.6 whole).
+I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, double chunk_us) {
     I8Plan p{};
     p.full = (int)(tiles / workers);
     p.rem = (int)(tiles % workers);
     p.cuts = 1;
-    if (p.rem) p.cuts = (int)std::min<int64_t>({workers / p.rem, chunks, max_cuts(chunks, cols)});
-    p.workers = p.full ? workers : p.rem * p.cuts;
+    const double fix_us = 5.0 + 0.08 * (double)cols, tile_us = (double)chunks * chunk_us;
+    if (p.rem) {
+        const int n = (int)std::min<int64_t>({workers / p.rem, chunks, max_cuts(chunks, cols)});
+        if (n > 1 && tile_us * (n - 1) / n > fix_us) p.cuts = n;
+        if (workers / p.rem == 1 && tile_us * (workers - p.rem) / workers > fix_us) p.cuts = 0;
+    }
+    p.workers = p.full || p.cuts == 0 ? workers : p.rem * p.cuts;
     return p;
 }
-inline I8Plan stream_plan(int64_t M, int64_t N, int64_t K, int nw) {
-    const int nt = stream_nt(M);
-    return make_plan(div_up(M, nt) * div_up(N, 128), div_up(K, I8_KC), std::min<int64_t>(M, nt) * nw, kSMs);
+
+// Which kernel makes a product, and how.
+struct ProductPlan {
+    int nt;        // tokens per tile of k_i8_stream; 0: k_i8_tile
+    I8Plan work;   // (k_i8_stream)
+};
+// The smaller estimate, in us, of what was measured on shapes from 1 to 512
+// tokens and 1000 to 28672 channels (within 15%): a CTA of k_i8_stream takes
+// 0.0115 a KB of stage, 0.21 at least, unless HBM needs longer for the weights
+// (6.2 TB/s), and cuts cost 5 + 0.08 a column; k_i8_tile takes 0.36 a stage of
+// its 256 x 256 tiles.  Few tokens per tile make more tiles where there are
+// few channels (64 tokens, 4096 x 4096: 11.3 us with 16, 12.9 with 64), many
+// read the weights once (14336 x 4096 gated: 60 us with 16, 25 with 64).
+ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
+    const int64_t chunks = div_up(K, I8_KC);
+    const int64_t tiles = div_up(M, 256) * div_up(N, 256 / nw);
+    ProductPlan best{0, {}};
+    double best_us = 7.0 + (double)(div_up(tiles, kPairs) * chunks) * 0.36;
+    const double hbm_us = (double)N * (double)K * nw / 6.2e6;
+    for (int nt = 16; nt <= 128; nt *= 2) {
+        if (nt > 16 && nt >= 2 * M) break;
+        const int64_t t = div_up(M, nt) * div_up(N, 128), cols = std::min<int64_t>(M, nt) * nw;
+        if (t > 16 * kSMs) continue;   // far into k_i8_tile's range
+        const I8Plan p = make_plan(t, chunks, cols, kSMs, 0.28 * nw);
+        const double stage_us = std::max(0.21, 0.0115 * (16 * nw + nt / 8));
+        const double each = (double)p.full * chunks +
+                            (p.rem == 0 ? 0.0 : p.cuts == 0 ? (double)p.rem * chunks / kSMs : (double)chunks / p.cuts);
+        const double us = std::max(hbm_us, each * stage_us) + 4.0 + 0.02 * cols +
+                          (p.cuts == 1 ? 0.0 : 5.0 + 0.08 * cols);
+        if (us < best_us) {
+            best_us = us;
+            best = {nt, p};
+        }
+    }
+    return best;
 }
 inline I8Plan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
     const int nt = dx_nt(M), u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
-    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs);
+    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs, 0.3);
+}
+inline int64_t plan_slots(const I8Plan& p) {
+    return p.cuts == 0 ? 2 * p.workers : p.cuts == 1 ? 0 : (int64_t)p.rem * p.cuts;
 }
 
-// Partial sums: a slot a worker with a piece of a cut tile, 128 lanes x NT columns.
+// Partial sums: 128 lanes x NT columns a slot.
 inline size_t product_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    if (M > kStreamMaxM) return 0;
-    const I8Plan p = stream_plan(M, N, K, nw);
-    return p.cuts < 2 ? 0 : (size_t)p.rem * p.cuts * nw * stream_nt(M) * 128 * 4;
+    const ProductPlan p = product_plan(M, N, K, nw);
+    return p.nt == 0 ? 0 : (size_t)plan_slots(p.work) * nw * p.nt * 128 * 4;
 }
 inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    const I8Plan p = dx_plan(M, N, K, nw);
-    return p.cuts < 2 ? 0 : (size_t)p.rem * p.cuts * 2 * dx_nt(M) * 128 * 4;
+    return (size_t)plan_slots(dx_plan(M, N, K, nw)) * 2 * dx_nt(M) * 128 * 4;
 }
 
 inline int64_t grad_ld(int64_t n) { return div_up(n, 64) * 64; }
@@ -312,12 +338,11 @@ mpq_status launch_big(dim3 grid, int threads, size_t smem, void* stream, Args&&.
 }
 
 template <int NT, int MODE, int ACT>
-mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& p, void* stream) {
+mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& p, const I8Plan& plan, void* stream) {
     constexpr int NW = MODE == 0 ? 1 : 2;
     CUtensorMap xm, w0, w1;
     if (!make_map(&xm, x, NT, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
         return MPQ_ERR_CUDA;
-    const I8Plan plan = stream_plan(p.M, p.N, p.K, NW);
     return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)plan.workers), I8S_WARPS * 32,
                                                   sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p, plan);
 }
@@ -344,12 +369,13 @@ mpq_status product_run(const mpq_i8* x, const mpq_i8* const* w, I8Product& p, co
     p.err = ws.err;
     p.counters = ws.counters;
     p.slots = static_cast<int32_t*>(ws.slots);
-    if (p.M > kStreamMaxM) return tile_run<MODE, ACT>(x, w, p, stream);
-    switch (stream_nt(p.M)) {
-        case 16: return stream_run<16, MODE, ACT>(x, w, p, stream);
-        case 32: return stream_run<32, MODE, ACT>(x, w, p, stream);
-        case 64: return stream_run<64, MODE, ACT>(x, w, p, stream);
-        default: return stream_run<128, MODE, ACT>(x, w, p, stream);
+    const ProductPlan plan = product_plan(p.M, p.N, p.K, MODE == 0 ? 1 : 2);
+    switch (plan.nt) {
+        case 0: return tile_run<MODE, ACT>(x, w, p, stream);
+        case 16: return stream_run<16, MODE, ACT>(x, w, p, plan.work, stream);
+        case 32: return stream_run<32, MODE, ACT>(x, w, p, plan.work, stream);
+        case 64: return stream_run<64, MODE, ACT>(x, w, p, plan.work, stream);
+        default: return stream_run<128, MODE, ACT>(x, w, p, plan.work, stream);
     }
 }
 
