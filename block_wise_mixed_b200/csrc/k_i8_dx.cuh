@@ -8,7 +8,7 @@
 // tokens over the two SMs of a cluster.
 //
 // The codes lie with k along the rows and the contraction across them; the
-// operand wants the contraction along its rows, in bf16.  Eight warps turn
+// operand wants the contraction along its rows, in bf16.  Converter warps turn
 // each 64 x 128 block of codes (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
 // one byte permute, and makes them bf16 with two masks and one subtraction:
@@ -21,9 +21,9 @@
 // cut tile are added in the order of the pieces by the last contributor,
 // whoever that is, so results are reproducible.
 //
-// Roles: warp 0 copies the codes and warp 18 the tokens, each as far ahead as
-// its own stages allow; warp 1 of the first CTA issues, warps 2-9 finish
-// (lane = k column), warps 10-17 convert.  Every wait is bounded.
+// Roles: warp 0 copies the codes and the last warp the tokens, each as far ahead
+// as its own stages allow; warp 1 of the first CTA issues, the EPI warps from 2
+// on finish (lane = k column), the rest convert.  Every wait is bounded.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -31,10 +31,8 @@
 
 namespace mpq {
 
-constexpr int I8X_GROUPS = 2;               // converter groups, a stage each in turn
-constexpr int I8X_GWARPS = 4;               // warps of a group
-constexpr int I8X_EPI = 8;                  // two for each TMEM lane quadrant
-constexpr int I8X_WARPS = 3 + I8X_EPI + I8X_GROUPS * I8X_GWARPS;
+constexpr int I8X_GWARPS = 4;               // warps of a converter group
+constexpr int I8X_MAX_EPI = 8;
 constexpr int I8X_NC = 64;                  // channels in a stage
 constexpr int I8X_RAW = I8X_NC * 128;       // codes of a stage
 constexpr int I8X_A = 128 * I8X_NC * 2;     // converted
@@ -51,6 +49,11 @@ struct I8DxCfg {
     static constexpr int S = NT == 256 ? 5 : 3;                // operand stages
     static constexpr int R = NT == 256 ? 6 : NT == 128 ? 3 : NT == 64 ? 5 : 6;   // code stages
     static constexpr uint32_t COLS = 2 * NT;                   // double-buffered accumulator
+    // Finishing warps, 32 columns each in turn, and converter groups, which
+    // take stages in turn: 19 warps leave a thread 96 registers.
+    static constexpr int EPI = NT == 32 ? 4 : 8;
+    static constexpr int GROUPS = NT == 32 ? 3 : 2;
+    static constexpr int WARPS = 3 + EPI + GROUPS * I8X_GWARPS;
 };
 
 template <int NT>
@@ -85,13 +88,13 @@ __device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j
 }
 
 template <int NT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8X_WARPS * 32, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(I8DxCfg<NT>::WARPS * 32, 1)
 k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
         const __grid_constant__ CUtensorMap gmap0, const __grid_constant__ CUtensorMap gmap1, I8DxParams p,
         I8Plan plan) {
     using Cfg = I8DxCfg<NT>;
-    constexpr int S = Cfg::S, R = Cfg::R, U = Cfg::U;
-    static_assert(R >= S && S >= I8X_GROUPS, "the converters' parity waits");
+    constexpr int S = Cfg::S, R = Cfg::R, U = Cfg::U, EPI = Cfg::EPI, GROUPS = Cfg::GROUPS;
+    static_assert(R >= S && S >= Cfg::GROUPS, "the converters' parity waits");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     I8DxSmem<NT>& sm = *reinterpret_cast<I8DxSmem<NT>*>(base);
@@ -115,7 +118,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.d_full[b], 1);
-            mbar_init(&sm.d_empty[b], 2 * I8X_EPI);
+            mbar_init(&sm.d_empty[b], 2 * Cfg::EPI);
         }
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
@@ -164,7 +167,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         }
         if (!ok && issuer) timed_out();
         __syncwarp();
-    } else if (warp == I8X_WARPS - 1) {
+    } else if (warp == Cfg::WARPS - 1) {
         const bool issuer = elect_one();
         const uint32_t full0 = cluster_addr(&sm.full[0], 0);
         int s = 0;
@@ -231,8 +234,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             if (!ok && issuer) timed_out();
         }
         __syncwarp();
-    } else if (warp < 2 + I8X_EPI) {
-        const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 64
+    } else if (warp < 2 + EPI) {
+        const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 8 EPI
         const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
         for (int seg = 0; seg < n_segs; ++seg) {
             const I8Seg g = work.seg(seg);
@@ -253,7 +256,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
-            uint32_t* counter = p.counters + (c0 * 2 + rank) * I8X_EPI + warp - 2;
+            uint32_t* counter = p.counters + (c0 * 2 + rank) * EPI + warp - 2;
             const uint32_t others = (uint32_t)(c1 - c0);
             bool mine = 32 * half < mc;
             if (mine && c0 != c1) {
@@ -261,7 +264,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 if (lane == 0) seen = i8_load_acquire(counter);
                 if (__shfl_sync(0xffffffffu, seen, 0) != others) {
                     float* slot = slot_of(pair);
-                    for (int c = 32 * half; c < mc; c += 64) {
+                    for (int c = 32 * half; c < mc; c += 8 * EPI) {
                         uint32_t r[32];
                         i8_tmem_ld32(taddr + (uint32_t)c, r);
                         i8_tmem_wait();
@@ -280,7 +283,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 }
             }
             if (mine) {
-                for (int c = 32 * half; c < mc; c += 64) {
+                for (int c = 32 * half; c < mc; c += 8 * EPI) {
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -318,11 +321,11 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
             if (lane == 0) cluster_arrive(empty_bar + 8u * (uint32_t)buf);
         }
     } else {
-        // converters: a group takes every other stage, so that two stages'
+        // converters: the groups take the stages in turn, so that several stages'
         // waits, loads and fences overlap.  Warp q of it takes rows 0 .. 31,
         // then 32 .. 63; lane (c, g) the eight rows of block c and the four
         // columns of group (g + 8 c + 8 q) % 32
-        const int group = (warp - 2 - I8X_EPI) / I8X_GWARPS, q = (warp - 2 - I8X_EPI) % I8X_GWARPS, c = lane & 3;
+        const int group = (warp - 2 - EPI) / I8X_GWARPS, q = (warp - 2 - EPI) % I8X_GWARPS, c = lane & 3;
         const int kg = ((lane >> 2) + 8 * c + 8 * q) & 31;
         uint32_t at[4];   // chunk of column 4 kg + j, block c (block c + 4: the other half of the row)
 #pragma unroll
@@ -338,7 +341,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         }
         // stage and phase of this group's unit in either ring
         uint32_t r = group, s = group, rph = 0, sph = 1;
-        for (uint32_t it = group; it < n_units; it += I8X_GROUPS) {
+        for (uint32_t it = group; it < n_units; it += GROUPS) {
             // The operand stage first: a parity wait can tell a phase only from
             // its neighbour.  Units up to it - S are multiplied once empty[s]
             // says so, so (R >= S) the copy of unit it - R has landed and
@@ -372,9 +375,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 mbar_arrive(&sm.raw_empty[r]);
                 cluster_arrive(full0 + 8u * s);
             }
-            r += I8X_GROUPS;
+            r += GROUPS;
             if (r >= R) { r -= R; rph ^= 1u; }
-            s += I8X_GROUPS;
+            s += GROUPS;
             if (s >= S) { s -= S; sph ^= 1u; }
         }
     }
@@ -402,35 +405,50 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 // ---------------------------------------------------------------------------
 // g = dy * scale of its channel, rounded to bf16 (the operand above).
 // ---------------------------------------------------------------------------
+// A thread keeps its columns' scales and goes down the rows.
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64_t lddy, const float* s, uint16_t* g,
                                                        int64_t ldg, int M, int N) {
+    constexpr int PER = VEC ? 8 : 2;
+    const int n = (blockIdx.x * 256 + threadIdx.x) * PER;   // g's rows are padded to 64
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int PER = VEC ? 8 : 2;
-    const int cols = (N + PER - 1) / PER;   // g's rows are padded to 64
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)M * cols; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / cols;
-        const int n = (int)(i % cols) * PER;
-        const uint16_t* d = dy + m * lddy + n;
-        float v[PER];
-        if (VEC && n + PER <= N) {
-            const uint4 u = *reinterpret_cast<const uint4*>(d);
-            float f[8];
-            I8Elem<true>::unpack(u, f);
+    if (n >= N) return;
+    float sc[PER];
 #pragma unroll
-            for (int j = 0; j < PER; ++j) v[j] = f[j] * s[n + j];
-        } else {
+    for (int j = 0; j < PER; ++j) sc[j] = n + j < N ? s[n + j] : 0.f;
+    const bool whole = n + PER <= N;
+    for (int m0 = blockIdx.y * 4; m0 < M; m0 += gridDim.y * 4) {
+        uint32_t w[4][PER / 2];   // four rows' gradients in flight
 #pragma unroll
-            for (int j = 0; j < PER; ++j) v[j] = n + j < N ? I8Elem<true>::get(d[j]) * s[n + j] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < PER / 2; ++j) w[i][j] = 0u;
+            if (m0 + i < M) {
+                const uint16_t* d = dy + (int64_t)(m0 + i) * lddy + n;
+                if (VEC && whole) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(d);
+                    w[i][0] = u.x;
+                    w[i][PER > 2 ? 1 : 0] = u.y;
+                    w[i][PER > 4 ? 2 : 0] = u.z;
+                    w[i][PER > 6 ? 3 : 0] = u.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        if (n + j < N) w[i][j / 2] |= (uint32_t)d[j] << (16 * (j & 1));
+                }
+            }
         }
-        uint32_t* o = reinterpret_cast<uint32_t*>(g + m * ldg + n);
-        if (VEC)
-            *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[PER > 3 ? 3 : 1]),
-                                                      pack_bf16(v[PER > 4 ? 4 : 0], v[PER > 5 ? 5 : 1]),
-                                                      pack_bf16(v[PER > 6 ? 6 : 0], v[PER > 7 ? 7 : 1]));
-        else
-            *o = pack_bf16(v[0], v[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (m0 + i >= M) break;
+            uint32_t o[PER / 2];
+#pragma unroll
+            for (int j = 0; j < PER / 2; ++j) o[j] = pack_bf16(bf16_lo(w[i][j]) * sc[2 * j], bf16_hi(w[i][j]) * sc[2 * j + 1]);
+            uint32_t* out = reinterpret_cast<uint32_t*>(g + (int64_t)(m0 + i) * ldg + n);
+            if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[PER > 2 ? 1 : 0], o[PER > 4 ? 2 : 0], o[PER > 6 ? 3 : 0]);
+            else *out = o[0];
+        }
     }
 }
 

@@ -159,7 +159,7 @@ constexpr int kPairs = kSMs / 2;
 // mpq_i8_* calls, so one workspace serves them all, one after another.
 constexpr size_t kErrBytes = 256;
 constexpr size_t kI8ZeroBytes = kErrBytes + 9728;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
-static_assert(kSMs * I8S_EPI * 4 <= 9728 && kPairs * 2 * I8X_EPI * 4 <= 9728 && kI8ZeroBytes % 256 == 0, "counters");
+static_assert(kSMs * I8S_EPI * 4 <= 9728 && kPairs * 2 * I8X_MAX_EPI * 4 <= 9728 && kI8ZeroBytes % 256 == 0, "counters");
 
 inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
@@ -388,7 +388,7 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
         !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
     const I8Plan plan = dx_plan(p.M, p.N, p.K, nw);
-    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * plan.workers)), I8X_WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
+    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * plan.workers)), I8DxCfg<NT>::WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
                                    stream, w0, w1, g0, g1, p, plan);
 }
 
@@ -479,11 +479,11 @@ mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M
     if (st != MPQ_OK) return st;
     const int64_t ldg = grad_ld(w->rows);
     const bool vec = aligned(dy_dev, 16) && (M == 1 || lddy % 8 == 0);
-    const unsigned blocks = (unsigned)std::min<int64_t>(div_up((int64_t)M * ldg / (vec ? 8 : 2), 256), kSMs * 8);
+    const int64_t gx = div_up(w->rows, 256 * (vec ? 8 : 2));
+    const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(div_up(M, 4), kSMs * 8 / gx)));
     const uint16_t* dy = static_cast<const uint16_t*>(dy_dev);
-    st = vec ? launch(k_i8_scale_grad<true>, dim3(blocks), 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows)
-             : launch(k_i8_scale_grad<false>, dim3(blocks), 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M,
-                      w->rows);
+    st = vec ? launch(k_i8_scale_grad<true>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows)
+             : launch(k_i8_scale_grad<false>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows);
     if (st != MPQ_OK) return st;
     return dx_run(&w, 1, k.grads, ldg, 0, M, dx_dev, lddx, k, stream);
 }
