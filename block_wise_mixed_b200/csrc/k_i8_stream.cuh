@@ -50,7 +50,7 @@ struct I8StreamSmem {
     using Cfg = I8StreamCfg<NT, NW>;
     uint8_t st[Cfg::STAGES][Cfg::STAGE];              // 1024-aligned
     uint64_t full[Cfg::STAGES], empty[Cfg::STAGES];
-    uint64_t d_full[2], d_empty[2], drain;
+    uint64_t d_full[2], d_empty[2], drain, parts;
     uint32_t tmem;
     volatile int abort_flag;
 };
@@ -166,6 +166,7 @@ struct I8Column {
 // cuts = 0 as equal runs over all their chunks.
 struct I8Plan {
     int full, rem, cuts, workers;
+    int cluster;   // the pieces of a tile are the CTAs of a cluster (k_i8_stream, full = 0)
 };
 // A worker's j-th segment: a tile, its chunks [k0, k1), and the contributors
 // c0 .. c1 to that tile.
@@ -251,6 +252,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             mbar_init(&sm.d_empty[b], I8S_EPI);
         }
         mbar_init(&sm.drain, 1);
+        mbar_init(&sm.parts, (uint32_t)(max(plan.cuts, 1) * I8S_EPI));
         sm.abort_flag = 0;
         fence_mbar_init();
         i8_tma_prefetch(&xmap);
@@ -260,6 +262,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
     if (warp == 1) i8_tmem_alloc<false>(&sm.tmem, Cfg::COLS);
     i8_fence_before();
     __syncthreads();
+    if (plan.cluster) cluster_sync();   // the peers' barriers are ready
     i8_fence_after();
     const uint32_t tmem = sm.tmem;
     pdl_wait();
@@ -351,41 +354,16 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             auto slot_of = [&](int c) {
                 return p.slots + (size_t)work.slot(c, c0) * (NW * NT * 128) + quad * 32 + lane;
             };
-            // A cut tile: when all others have arrived already, this one only
-            // adds; else it leaves its part and counts itself in.
-            uint32_t* counter = p.counters + c0 * I8S_EPI + warp - 2;
-            const uint32_t others = (uint32_t)(c1 - c0);
-            bool mine = 8 * part < mc;   // this warp writes the results
-            if (mine && c0 != c1) {
-                uint32_t seen = 0;
-                if (lane == 0) seen = i8_load_acquire(counter);
-                if (__shfl_sync(0xffffffffu, seen, 0) != others) {
-                    int32_t* slot = slot_of(cta);
-                    for (int c = 8 * part; c < mc; c += 32) {
-                        uint32_t r[NW][8];
+            // This CTA's sums of columns c .. c + 7, and the outputs of eight
+            // columns.  What the outputs need is loaded first (a store may
+            // alias it for all the compiler knows, and each load would wait
+            // for the store before).
+            auto own_sums = [&](int c, uint32_t (&r)[NW][8]) {
 #pragma unroll
-                        for (int j = 0; j < NW; ++j) i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r[j]);
-                        i8_tmem_wait();
-#pragma unroll
-                        for (int j = 0; j < NW; ++j)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[j][i];
-                    }
-                    __threadfence();
-                    __syncwarp();
-                    if (lane == 0) seen = atomic_add_acq_rel_gpu(counter, 1u);
-                    mine = __shfl_sync(0xffffffffu, seen, 0) == others;
-                }
-                if (mine) {
-                    if (lane == 0) *counter = 0u;   // clean for the next call
-                    __threadfence();
-                }
-            }
-            // Eight columns at a time: the sums, then the outputs.  Loads come
-            // first (a store may alias them for all the compiler knows, and
-            // each would wait for the one before), two contributors' together.
-            for (int c = 8 * part; mine && c < mc; c += 32) {
+                for (int j = 0; j < NW; ++j) i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r[j]);
+                i8_tmem_wait();
+            };
+            auto finish = [&](int c, auto&& sums) {
                 const int left = mc - c;
                 float xs[8], dh[MODE == 2 ? 8 : 1];
 #pragma unroll
@@ -395,37 +373,115 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dh[MODE == 2 ? i : 0] = i < left ? col.next_dh() : 0.f;
                 int acc[NW][8] = {};
-                if (c0 != c1)
-                    for (int o = c0; o <= c1; o += 2) {
-                        int t[2][NW][8];
+                sums(c, left, acc);
+                I8Value o[8];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const bool add = o + q <= c1 && o + q != cta;
-                            const int32_t* slot = slot_of(o + q);
+                for (int i = 0; i < 8; ++i)
+                    o[i] = i8_value<MODE, ACT>(acc[0][i], acc[NW - 1][i], ws0, ws1, xs[i], dh[MODE == 2 ? i : 0]);
+                if (in) col.put(o, left);
+                __syncwarp();
+            };
+            if (c0 != c1 && plan.cluster) {
+                // columns go to part + lane of [NW NT][128] words in every CTA's first stages
+                const uint32_t part0 = smem_u32(sm.st[0]) + (uint32_t)(quad * 32 + lane) * 4u;
+                for (int c = 8 * part; c < mc; c += 32) {
+                    uint32_t r[NW][8];
+                    own_sums(c, r);
+#pragma unroll
+                    for (int j = 0; j < NW; ++j)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(part0 + (uint32_t)(j * NT + c + i) * 512u), "r"(r[j][i])
+                                         : "memory");
+                }
+                __syncwarp();
+                if (lane < plan.cuts) cluster_arrive_release(cluster_addr(&sm.parts, (uint32_t)lane));
+                if (!__all_sync(0xffffffffu, i8_wait<true>(&sm.parts, 0u))) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                const int rank = cta - c0, step = 8 * plan.cuts;
+                for (int c = 8 * rank + step * part; c < mc; c += 4 * step)
+                    finish(c, [&](int c, int, int (&acc)[NW][8]) {
+                        for (int o = 0; o < plan.cuts; o += 4 / NW) {   // some peers' loads in flight
+                            uint32_t t[4 / NW][NW][8];
+#pragma unroll
+                            for (int q = 0; q < 4 / NW; ++q) {
+                                const uint32_t peer = cluster_map(part0, (uint32_t)min(o + q, plan.cuts - 1));
+#pragma unroll
+                                for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) t[q][j][i] = cluster_load(peer + (uint32_t)(j * NT + c + i) * 512u);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4 / NW; ++q)
+                                if (o + q < plan.cuts)
+#pragma unroll
+                                    for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) acc[j][i] += (int)t[q][j][i];
+                        }
+                    });
+            } else {
+                // A tile cut between CTAs that are no cluster: when all others
+                // have arrived already, this one only adds; else it leaves its
+                // part and counts itself in.
+                uint32_t* counter = p.counters + c0 * I8S_EPI + warp - 2;
+                const uint32_t others = (uint32_t)(c1 - c0);
+                bool mine = 8 * part < mc;   // this warp writes the results
+                if (mine && c0 != c1) {
+                    uint32_t seen = 0;
+                    if (lane == 0) seen = i8_load_acquire(counter);
+                    if (__shfl_sync(0xffffffffu, seen, 0) != others) {
+                        int32_t* slot = slot_of(cta);
+                        for (int c = 8 * part; c < mc; c += 32) {
+                            uint32_t r[NW][8];
+                            own_sums(c, r);
 #pragma unroll
                             for (int j = 0; j < NW; ++j)
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
-                                    t[q][j][i] = add && i < left ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
+                                    if (c + i < mc) slot[(j * NT + c + i) * 128] = (int)r[j][i];
                         }
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int j = 0; j < NW; ++j)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) acc[j][i] += t[q][j][i];
+                        __threadfence();
+                        __syncwarp();
+                        if (lane == 0) seen = atomic_add_acq_rel_gpu(counter, 1u);
+                        mine = __shfl_sync(0xffffffffu, seen, 0) == others;
                     }
-                uint32_t r[NW][8];
+                    if (mine) {
+                        if (lane == 0) *counter = 0u;   // clean for the next call
+                        __threadfence();
+                    }
+                }
+                for (int c = 8 * part; mine && c < mc; c += 32)
+                    finish(c, [&](int c, int left, int (&acc)[NW][8]) {
+                        if (c0 != c1)
+                            for (int o = c0; o <= c1; o += 2) {   // two contributors' loads in flight
+                                int t[2][NW][8];
 #pragma unroll
-                for (int j = 0; j < NW; ++j) i8_tmem_ld8(taddr + (uint32_t)(j * NT + c), r[j]);
-                i8_tmem_wait();
-                I8Value o[8];
+                                for (int q = 0; q < 2; ++q) {
+                                    const bool add = o + q <= c1 && o + q != cta;
+                                    const int32_t* slot = slot_of(o + q);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = i8_value<MODE, ACT>(acc[0][i] + (int)r[0][i], acc[NW - 1][i] + (int)r[NW - 1][i], ws0, ws1,
-                                               xs[i], dh[MODE == 2 ? i : 0]);
-                if (in) col.put(o, left);
-                __syncwarp();
+                                    for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i)
+                                            t[q][j][i] = add && i < left ? __ldcg(slot + (j * NT + c + i) * 128) : 0;
+                                }
+#pragma unroll
+                                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                    for (int j = 0; j < NW; ++j)
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) acc[j][i] += t[q][j][i];
+                            }
+                        uint32_t r[NW][8];
+                        own_sums(c, r);
+#pragma unroll
+                        for (int j = 0; j < NW; ++j)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) acc[j][i] += (int)r[j][i];
+                    });
             }
             i8_fence_before();
             __syncwarp();
@@ -444,8 +500,10 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             i8_wait_warp(&sm.drain, 0u);
         }
     }
+    if (sm.abort_flag && plan.cluster) i8_settle();
     i8_fence_before();
     __syncthreads();
+    if (plan.cluster) cluster_sync();   // nobody reads this CTA's part any more
     if (warp == 1) {
         i8_fence_after();
         i8_tmem_free<false>(tmem, Cfg::COLS);

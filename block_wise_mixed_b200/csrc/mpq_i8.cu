@@ -54,18 +54,25 @@ mpq_status check_ws(const void* ws, size_t have, size_t need) {
 // dependent launch).  The kernels read and write global memory only after
 // griddepcontrol.wait, and let their dependents start only after it.
 template <typename... KArgs, typename... Args>
-mpq_status launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, void* stream, Args&&... args) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+mpq_status launch_cluster(int cluster, void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, void* stream,
+                          Args&&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = static_cast<cudaStream_t>(stream);
-    c.attrs = pdl;
-    c.numAttrs = 1;
+    c.attrs = attr;
+    c.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, std::forward<Args>(args)...) == cudaSuccess ? MPQ_OK : MPQ_ERR_CUDA;
+}
+template <typename... KArgs, typename... Args>
+mpq_status launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, void* stream, Args&&... args) {
+    return launch_cluster(0, kernel, grid, threads, smem, stream, std::forward<Args>(args)...);
 }
 
 // ---------------------------------------------------------------------------
@@ -174,16 +181,33 @@ inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 12
 inline int64_t max_cuts(int64_t chunks, int64_t cols) {
     return std::max<int64_t>(1, (int64_t)std::ceil(std::sqrt(14.0 * (double)chunks / (double)cols)));
 }
+// What it costs to add up a tile between the CTAs of a cluster.
+inline double cluster_fix_us(int64_t cols) { return 2.0 + 0.02 * (double)cols; }
+
 // chunk_us: a stage's time.  Cuts, or equal runs, only where the time they take
 // off is worth more than a fix-up, about 5 us and 0.08 us a column (measured:
 // 16-token gradient of 8192 x 28672, 112 tiles on 74 pairs: 55 us in runs, 62
 // whole; one token through 14336 x 4096: 16.8 us in runs, 13.6 whole).
-I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, double chunk_us) {
+I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, double chunk_us, bool clusters) {
     I8Plan p{};
     p.full = (int)(tiles / workers);
     p.rem = (int)(tiles % workers);
     p.cuts = 1;
     const double fix_us = 5.0 + 0.08 * (double)cols, tile_us = (double)chunks * chunk_us;
+    if (clusters && p.full == 0 && workers / p.rem >= 2) {
+        // All clusters at once: the occupancy query gives 74, 45, 33, 26, 22, 15
+        // and 15 clusters of 2 to 8 CTAs; a few less here, as a second wave
+        // costs more than smaller clusters (2048 x 2048: 10.7 us in 16 of 8).
+        static const int kFit[9] = {0, 0, 72, 44, 32, 24, 20, 14, 14};
+        int n = (int)std::min<int64_t>({workers / p.rem, chunks, 8});
+        while (n > 1 && kFit[n] < p.rem) --n;
+        if (n > 1 && tile_us * (n - 1) / n > cluster_fix_us(cols)) {
+            p.cuts = n;
+            p.cluster = 1;
+            p.workers = p.rem * n;
+            return p;
+        }
+    }
     if (p.rem) {
         const int n = (int)std::min<int64_t>({workers / p.rem, chunks, max_cuts(chunks, cols)});
         if (n > 1 && tile_us * (n - 1) / n > fix_us) p.cuts = n;
@@ -215,12 +239,12 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
         if (nt > 16 && nt >= 2 * M) break;
         const int64_t t = div_up(M, nt) * div_up(N, 128), cols = std::min<int64_t>(M, nt) * nw;
         if (t > 16 * kSMs) continue;   // far into k_i8_tile's range
-        const I8Plan p = make_plan(t, chunks, cols, kSMs, 0.28 * nw);
+        const I8Plan p = make_plan(t, chunks, cols, kSMs, 0.28 * nw, true);
         const double stage_us = std::max(0.21, 0.0115 * (16 * nw + nt / 8));
         const double each = (double)p.full * chunks +
                             (p.rem == 0 ? 0.0 : p.cuts == 0 ? (double)p.rem * chunks / kSMs : (double)chunks / p.cuts);
         const double us = std::max(hbm_us, each * stage_us) + 4.0 + 0.02 * cols +
-                          (p.cuts == 1 ? 0.0 : 5.0 + 0.08 * cols);
+                          (p.cuts == 1 ? 0.0 : p.cluster ? cluster_fix_us(cols) : 5.0 + 0.08 * cols);
         if (us < best_us) {
             best_us = us;
             best = {nt, p};
@@ -230,10 +254,10 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
 }
 inline I8Plan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
     const int nt = dx_nt(M), u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
-    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs, 0.3);
+    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs, 0.3, false);
 }
 inline int64_t plan_slots(const I8Plan& p) {
-    return p.cuts == 0 ? 2 * p.workers : p.cuts == 1 ? 0 : (int64_t)p.rem * p.cuts;
+    return p.cuts == 0 ? 2 * p.workers : p.cuts == 1 || p.cluster ? 0 : (int64_t)p.rem * p.cuts;
 }
 
 // Partial sums: 128 lanes x NT columns a slot.
@@ -324,7 +348,7 @@ bool make_map(CUtensorMap* map, const mpq_i8* q, int box_rows, bool swizzle) {
 
 // Launches with all the shared memory a kernel asks for (raised once per device).
 template <auto Kernel, typename... Args>
-mpq_status launch_big(dim3 grid, int threads, size_t smem, void* stream, Args&&... args) {
+mpq_status launch_big(int cluster, dim3 grid, int threads, size_t smem, void* stream, Args&&... args) {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MPQ_ERR_CUDA;
@@ -334,7 +358,7 @@ mpq_status launch_big(dim3 grid, int threads, size_t smem, void* stream, Args&&.
             return MPQ_ERR_CUDA;
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch(Kernel, grid, threads, smem, stream, std::forward<Args>(args)...);
+    return launch_cluster(cluster, Kernel, grid, threads, smem, stream, std::forward<Args>(args)...);
 }
 
 template <int NT, int MODE, int ACT>
@@ -343,7 +367,7 @@ mpq_status stream_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& 
     CUtensorMap xm, w0, w1;
     if (!make_map(&xm, x, NT, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
         return MPQ_ERR_CUDA;
-    return launch_big<k_i8_stream<NT, MODE, ACT>>(dim3((unsigned)plan.workers), I8S_WARPS * 32,
+    return launch_big<k_i8_stream<NT, MODE, ACT>>(plan.cluster ? plan.cuts : 0, dim3((unsigned)plan.workers), I8S_WARPS * 32,
                                                   sizeof(I8StreamSmem<NT, NW>) + 1024, stream, xm, w0, w1, p, plan);
 }
 
@@ -354,7 +378,7 @@ mpq_status tile_run(const mpq_i8* x, const mpq_i8* const* w, const I8Product& p,
     if (!make_map(&xm, x, 128, true) || !make_map(&w0, w[0], 128, true) || !make_map(&w1, w[NW - 1], 128, true))
         return MPQ_ERR_CUDA;
     const int64_t tiles = div_up(p.M, 256) * div_up(p.N, 256 / NW);
-    return launch_big<k_i8_tile<MODE, ACT>>(dim3((unsigned)(2 * std::min<int64_t>(kPairs, tiles))), I8T_WARPS * 32,
+    return launch_big<k_i8_tile<MODE, ACT>>(0, dim3((unsigned)(2 * std::min<int64_t>(kPairs, tiles))), I8T_WARPS * 32,
                                             sizeof(I8TileSmem<MODE>) + 1024, stream, xm, w0, w1, p);
 }
 
@@ -388,7 +412,7 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
         !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
     const I8Plan plan = dx_plan(p.M, p.N, p.K, nw);
-    return launch_big<k_i8_dx<NT>>(dim3((unsigned)(2 * plan.workers)), I8DxCfg<NT>::WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
+    return launch_big<k_i8_dx<NT>>(0, dim3((unsigned)(2 * plan.workers)), I8DxCfg<NT>::WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
                                    stream, w0, w1, g0, g1, p, plan);
 }
 
