@@ -378,8 +378,8 @@ mpq_status mpq_fold_orders(int32_t n, const int32_t* row_perm_a, const int32_t* 
 
 /* An int8 matrix in device memory: tokens of the activations or output
  * channels of the weights as rows.  codes is 16-byte aligned, rows are ld
- * bytes apart (ld a multiple of 16, >= cols; the bytes behind a row's last
- * column are neither read nor written), scales holds rows floats (4-byte
+ * bytes apart (ld a multiple of 16, >= cols, < 2^40; the bytes behind a row's
+ * last column are neither used nor written), scales holds rows floats (4-byte
  * aligned).  1 <= cols <= MPQ_I8_MAX_COLS: the products' sums of cols terms
  * of up to 128 * 128 are exact in 32 bits. */
 #define MPQ_I8_MAX_COLS 131071
@@ -417,8 +417,10 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
  * m * ldy + n (ldy >= N), aligned to its type.
  *   ws  device workspace of mpq_i8_linear_workspace_size(M, N, K) bytes,
  *       256-byte aligned, zero-filled before its first use: the same rules
- *       as mpq_linear's (left clean by every call without a device error;
- *       not shared by calls that may overlap).
+ *       as mpq_linear's (left clean by every call without a device error, so
+ *       zero it again only after one).  One workspace of the largest size may
+ *       serve all mpq_i8_* calls of a stream, one after another; calls that
+ *       may overlap need their own, and it is not shared with mpq_linear.
  * Results do not depend on how the work is split.  Host errors: ARG, SHAPE
  * (columns differ, sizes out of range), WORKSPACE; device (mpq_check):
  * TIMEOUT.  M == 0 is a no-op. */
@@ -449,8 +451,9 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
  *   dx = sum_f (d_gate s_gate) gate.codes + (d_up s_up) up.codes   (M x K)
  *   d_gate and d_up (for adapters next to the frozen layers) may both be
  *   NULL; dx's products round the fp32 values, not the bf16 outputs.
- * Workspace rules and errors as for mpq_i8_linear.  Outputs must not overlap
- * inputs. */
+ * Sums are added in an order that the sizes fix: the same call gives the same
+ * bits.  Workspace rules and errors as for mpq_i8_linear.  Outputs must not
+ * overlap inputs. */
 size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K);
 mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M, int64_t lddy,
                                   void* dx_dev, int64_t lddx, void* ws, size_t ws_bytes, void* stream);

@@ -202,6 +202,44 @@ def test_linear(mpq, M, N, K):
             assert guards_ok(buf, M, N)
 
 
+# (operator, tokens, channels, columns): tile counts for each way that work is
+# handed out -- clusters of 2 to 8 pieces, whole rounds and cut remainders, equal
+# runs over the last round -- in the products and in the gradients
+WORK = [("linear", 1, 9000, 2048), ("linear", 3, 5000, 4096), ("linear", 2, 4000, 8192), ("linear", 5, 3000, 8192),
+        ("linear", 20, 2500, 4096), ("linear", 1, 1700, 4096), ("linear", 40, 900, 8192), ("linear", 100, 1000, 4096),
+        ("linear", 1, 21504, 4096), ("linear", 2, 9728, 16384), ("linear", 16, 19100, 6000), ("gated", 1, 9728, 8192),
+        ("gated", 30, 1000, 4096), ("gated", 9, 20900, 4096), ("gated", 90, 2000, 2048),
+        ("linear_backward", 16, 8192, 28672), ("linear_backward", 16, 8192, 512), ("linear_backward", 40, 5000, 900),
+        ("linear_backward", 600, 12000, 6656), ("linear_backward", 100, 3000, 20000), ("gated_backward", 20, 3000, 700)]
+
+
+@pytest.mark.parametrize("op,M,N,K", WORK)
+def test_work_distribution(mpq, op, M, N, K):
+    import torch
+    sc = 3.0 / (74.0 * 74.0 * K ** 0.5)
+    x, wg = rand_i8(mpq, M, K, 1), rand_i8(mpq, N, K, 2, sc)
+    wu = rand_i8(mpq, N, K, 3, sc) if "gated" in op else None
+    dh = (torch.randn(M, N, generator=gen(4), device="cuda") * 0.1).to(torch.bfloat16)
+    call = {"linear": lambda: (mpq.i8_linear(x, wg),), "gated": lambda: (mpq.i8_gated(x, wg, wu, ydtype=mpq.Y_F32),),
+            "linear_backward": lambda: (mpq.i8_linear_backward(wg, dh),),
+            "gated_backward": lambda: mpq.i8_gated_backward(x, wg, wu, dh)}[op]
+    got = call()
+    if op == "linear":
+        want = product64(x, wg)
+        assert_close(got[0], want, 3.01 * u * want.abs())
+    elif op == "gated":
+        a, b = product64(x, wg), product64(x, wu)
+        t, g, _, _ = gate64("silu", a)
+        assert_close(got[0], g * b, (20 + 15 * t.abs()) * u * 1.01 * (g * b).abs() + TINY * (1 + b.abs()))
+    elif op == "linear_backward":
+        assert_dx(got[0], *dx64([(dh.double(), u * dh.double().abs(), hat(wg))], N))
+    else:
+        wdg, wdu, tg, tu = grads64("silu", x, wg, wu, dh)
+        assert_dx(got[0], *dx64([(wdg, tg, hat(wg)), (wdu, tu, hat(wu))], 2 * N))
+    for _ in range(3):
+        assert same(call(), got)
+
+
 def test_linear_extreme_sums(mpq):
     """Sums next to the ends of int32 (every code -128 at the longest row), and
     scales whose product with the sum leaves fp32 only if the result does."""
