@@ -194,7 +194,7 @@ I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, doubl
     p.rem = (int)(tiles % workers);
     p.cuts = 1;
     const double fix_us = 5.0 + 0.08 * (double)cols, tile_us = (double)chunks * chunk_us;
-    if (clusters && p.full == 0 && workers / p.rem >= 2) {
+    if (clusters && p.full == 0 && p.rem > 0 && workers / p.rem >= 2) {   // (no tiles: an empty batch)
         // All clusters at once: the occupancy query gives 74, 45, 33, 26, 22, 15
         // and 15 clusters of 2 to 8 CTAs; a few less here, as a second wave
         // costs more than smaller clusters (2048 x 2048: 10.7 us in 16 of 8).

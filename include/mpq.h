@@ -381,7 +381,8 @@ mpq_status mpq_fold_orders(int32_t n, const int32_t* row_perm_a, const int32_t* 
  * bytes apart (ld a multiple of 16, >= cols, < 2^40; the bytes behind a row's
  * last column are neither used nor written), scales holds rows floats (4-byte
  * aligned).  1 <= cols <= MPQ_I8_MAX_COLS: the products' sums of cols terms
- * of up to 128 * 128 are exact in 32 bits. */
+ * of up to 128 * 128 are exact in 32 bits.  In all calls below outputs must
+ * not overlap inputs. */
 #define MPQ_I8_MAX_COLS 131071
 typedef struct {
     int32_t rows, cols;
@@ -400,6 +401,7 @@ typedef enum { MPQ_ACT_SILU = 0, MPQ_ACT_GELU_TANH = 1 } mpq_act;
  *   amax = max_c |x[r][c]|,  s = max(fl32(amax / 127), 2^-126), s = 1 if
  *   amax == 0;  code = the integer nearest to the exact quotient x / s, ties
  *   to even (within -127..127).
+ * What lies between the rows of x may be read, but is not used.
  * A row with a NaN or an infinity gets the scale NaN and codes 0, so that
  * what is computed from it is NaN and other rows are not touched.
  * Errors: ARG, SHAPE (rows < 0, cols out of range); rows == 0 is a no-op. */
@@ -452,8 +454,7 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
  *   d_gate and d_up (for adapters next to the frozen layers) may both be
  *   NULL; dx's products round the fp32 values, not the bf16 outputs.
  * Sums are added in an order that the sizes fix: the same call gives the same
- * bits.  Workspace rules and errors as for mpq_i8_linear.  Outputs must not
- * overlap inputs. */
+ * bits.  Workspace rules and errors as for mpq_i8_linear. */
 size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K);
 mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M, int64_t lddy,
                                   void* dx_dev, int64_t lddx, void* ws, size_t ws_bytes, void* stream);

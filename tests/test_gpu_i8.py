@@ -593,6 +593,65 @@ def test_weights_written_right_before(mpq):
         assert torch.equal(outs[r], ref[r % 3])
 
 
+def test_binding_refuses_tensors(mpq):
+    """Layouts, types and sizes that the calls do not take are refused, not read."""
+    import torch
+    x, w, w2 = rand_i8(mpq, 4, 64, 1), rand_i8(mpq, 8, 64, 2), rand_i8(mpq, 9, 64, 3)
+    dy = torch.zeros(4, 8, device="cuda", dtype=torch.bfloat16)
+    f = torch.zeros(4, 64, device="cuda")
+    bad = [
+        lambda: mpq.i8_quantize(f.t()), lambda: mpq.i8_quantize(f[:1].expand(4, 64)), lambda: mpq.i8_quantize(f.half()),
+        lambda: mpq.i8_quantize(f, out=w), lambda: mpq.i8_quantize(f.double()),
+        lambda: mpq.i8_matrix(x.codes[:, 1:], x.scales), lambda: mpq.i8_matrix(x.codes, x.scales[:3]),
+        lambda: mpq.i8_matrix(x.codes, x.scales.double()),
+        lambda: mpq.i8_matrix(torch.zeros(4, 20, device="cuda", dtype=torch.int8), x.scales),
+        lambda: mpq.i8_linear(x, rand_i8(mpq, 8, 65, 4)), lambda: mpq.i8_linear(x, w, out=torch.zeros(4, 9, device="cuda")),
+        lambda: mpq.i8_linear(x, w, out=torch.zeros(8, 4, device="cuda").t()), lambda: mpq.i8_linear(x.codes, w),
+        lambda: mpq.i8_linear(x, w, out=torch.zeros(4, 8, device="cuda", dtype=torch.float16)),
+        lambda: mpq.i8_linear(x, w, ws=torch.zeros(256, device="cuda", dtype=torch.uint8)),
+        lambda: mpq.i8_linear(x, w, ws=torch.zeros(1 << 20, device="cuda", dtype=torch.uint8)[16:]),
+        lambda: mpq.i8_gated(x, w, w2), lambda: mpq.i8_gated(x, w, w, act="relu"),
+        lambda: mpq.i8_linear_backward(w, dy.float()), lambda: mpq.i8_linear_backward(w2, dy),
+        lambda: mpq.i8_linear_backward(w, dy[:1].expand(4, 8)), lambda: mpq.i8_linear_backward(w, dy.t()),
+        lambda: mpq.i8_gated_backward(x, w, w, dy[:3]), lambda: mpq.i8_gated_backward(x, w, w2, dy),
+        lambda: mpq.i8_gated_backward(x, w, w, dy, d_gate=torch.zeros(4, 16, device="cuda", dtype=torch.bfloat16)[:, :8]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(mpq.MpqError):
+            call()
+            print("call %d was taken" % i)
+    # empty batches are no-ops
+    e = mpq.i8_quantize(torch.zeros(0, 64, device="cuda"))
+    assert mpq.i8_linear(e, w).shape == (0, 8) and mpq.i8_gated(e, w, w).shape == (0, 8)
+    assert mpq.i8_linear_backward(w, dy[:0]).shape == (0, 64)
+    assert [t.shape for t in mpq.i8_gated_backward(e, w, w, dy[:0])] == [(0, 64), (0, 8), (0, 8)]
+    assert mpq.i8_dequantize(e).shape == (0, 64)
+    # and the calls above left nothing behind
+    want = product64(x, w)
+    assert_close(mpq.i8_linear(x, w), want, 4 * u * want.abs())
+
+
+def test_two_streams_at_once(mpq):
+    """Calls that overlap on two streams, each with its own workspace."""
+    import torch
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = [ops(mpq, *s, 11 * i) for i, s in enumerate(((5, 3000, 4096), (300, 1371, 1001)))]
+    want = [[c() for _, c in calls] for calls in sets]
+    torch.cuda.synchronize()
+    spaces = [torch.zeros(64 << 20, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append([c(ws=spaces[i]) for _, c in sets[i]])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for rep in got[i]:
+            assert all(same(a, b) for a, b in zip(rep, want[i]))
+        mpq.check(spaces[i])
+
+
 def test_offsets_beyond_32_bits(mpq):
     """Codes beyond 2^31 bytes and outputs beyond 2^31 elements."""
     import torch
