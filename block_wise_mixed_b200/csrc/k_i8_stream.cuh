@@ -37,9 +37,13 @@ constexpr int I8_KC = 128;                            // bytes of k in a stage
 
 template <int NT, int NW>
 struct I8StreamCfg {
+    // 128-byte chunks of k in a stage: two of one matrix (a stage's waits,
+    // copies and commit cost each role some 400 cycles, as much as 18 KB take
+    // to arrive), one of two.
+    static constexpr int U = NW == 1 ? 2 : 1;
     static constexpr int W_BYTES = 128 * I8_KC;
     static constexpr int X_BYTES = NT * I8_KC;
-    static constexpr int STAGE = NW * W_BYTES + X_BYTES;
+    static constexpr int STAGE = U * (NW * W_BYTES + X_BYTES);
     static constexpr int STAGES = (204 * 1024) / STAGE;
     static constexpr int BUFS = NW * NT * 2 <= 512 ? 2 : 1;
     static constexpr uint32_t COLS = NW * NT * BUFS < 32 ? 32 : NW * NT * BUFS;
@@ -231,13 +235,13 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
             const __grid_constant__ CUtensorMap wmap1, I8Product p, I8Plan plan) {
     constexpr int NW = MODE == 0 ? 1 : 2;
     using Cfg = I8StreamCfg<NT, NW>;
-    constexpr int S = Cfg::STAGES, BUFS = Cfg::BUFS;
+    constexpr int S = Cfg::STAGES, BUFS = Cfg::BUFS, U = Cfg::U;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     I8StreamSmem<NT, NW>& sm = *reinterpret_cast<I8StreamSmem<NT, NW>*>(base);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    const int KB = (p.K + I8_KC - 1) / I8_KC;
+    const int KB = (p.K + U * I8_KC - 1) / (U * I8_KC);   // stages of a tile
     const int T = (p.N + 127) / 128, cta = blockIdx.x;
     const I8Work work(plan, cta, KB);
     const int n_segs = work.segs;
@@ -290,10 +294,14 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                     mbar_arrive_expect_tx(&sm.full[s], Cfg::STAGE);
                     if (!kI8WaitTest) {
                         const uint32_t bar = smem_u32(&sm.full[s]);
-                        const int kc = kb * I8_KC;
-                        i8_tma_load<false>(sm.st[s], &wmap0, kc, n0, bar);
-                        if (NW == 2) i8_tma_load<false>(sm.st[s] + Cfg::W_BYTES, &wmap1, kc, n0, bar);
-                        i8_tma_load<false>(sm.st[s] + NW * Cfg::W_BYTES, &xmap, kc, m0, bar);
+#pragma unroll
+                        for (int q = 0; q < U; ++q) {   // (a chunk behind the last reads as zeros)
+                            const int kc = (kb * U + q) * I8_KC;
+                            uint8_t* w = sm.st[s] + q * NW * Cfg::W_BYTES;
+                            i8_tma_load<false>(w, &wmap0, kc, n0, bar);
+                            if (NW == 2) i8_tma_load<false>(w + Cfg::W_BYTES, &wmap1, kc, n0, bar);
+                            i8_tma_load<false>(sm.st[s] + U * NW * Cfg::W_BYTES + q * Cfg::X_BYTES, &xmap, kc, m0, bar);
+                        }
                     }
                 }
                 if (kI8WaitTest) break;   // armed, no copy
@@ -322,9 +330,11 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                 const uint32_t st = smem_u32(sm.st[s]);
                 if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < NW; ++j)
-                        i8_mma4<false, 0>(tmem + (uint32_t)((buf * NW + j) * NT), st + j * Cfg::W_BYTES,
-                                          st + NW * Cfg::W_BYTES, idesc, i > 0);
+                    for (int q = 0; q < U; ++q)
+#pragma unroll
+                        for (int j = 0; j < NW; ++j)
+                            i8_mma4<false, 0>(tmem + (uint32_t)((buf * NW + j) * NT), st + (q * NW + j) * Cfg::W_BYTES,
+                                              st + U * NW * Cfg::W_BYTES + q * Cfg::X_BYTES, idesc, i > 0 || q > 0);
                     i8_commit<false>(&sm.empty[s]);
                     if (i == n - 1) i8_commit<false>(&sm.d_full[buf]);
                 }

@@ -222,28 +222,34 @@ struct ProductPlan {
     int nt;        // tokens per tile of k_i8_stream; 0: k_i8_tile
     I8Plan work;   // (k_i8_stream)
 };
-// The smaller estimate, in us, of what was measured on shapes from 1 to 512
-// tokens and 1000 to 28672 channels (within 15%): a CTA of k_i8_stream takes
-// 0.0115 a KB of stage, 0.21 at least, unless HBM needs longer for the weights
-// (6.2 TB/s), and cuts cost 5 + 0.08 a column; k_i8_tile takes 0.36 a stage of
-// its 256 x 256 tiles.  Few tokens per tile make more tiles where there are
-// few channels (64 tokens, 4096 x 4096: 11.3 us with 16, 12.9 with 64), many
-// read the weights once (14336 x 4096 gated: 60 us with 16, 25 with 64).
+// The smaller estimate, in us, fitted to what was measured on shapes from 1 to
+// 512 tokens and 1000 to 28672 channels: a stage of k_i8_stream takes 0.0078 a
+// KB, 0.30 at least (two chunks of one matrix), or 0.0115 a KB (one of two),
+// unless the weights take longer (6.2 TB/s from HBM, half as long from L2 for
+// each further tile of tokens); adding cut tiles up costs
+// what make_plan says; k_i8_tile takes 0.36 a chunk of its 256 x 256 tiles and
+// a quarter more than HBM's time.  Few tokens per tile make more tiles where
+// there are few channels (128 tokens, 4096 x 4096: 9.8 us with 32, 14.5 with 16,
+// 10.9 with 64 or 128), many read the weights once (64 tokens, 14336 x 4096:
+// 28.6 us with 16, 14.3 with 64).
 ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
-    const int64_t chunks = div_up(K, I8_KC);
+    const int u = nw == 1 ? I8StreamCfg<16, 1>::U : I8StreamCfg<16, 2>::U;
+    const int64_t chunks = div_up(K, u * I8_KC);
     const int64_t tiles = div_up(M, 256) * div_up(N, 256 / nw);
     ProductPlan best{0, {}};
-    double best_us = 7.0 + (double)(div_up(tiles, kPairs) * chunks) * 0.36;
     const double hbm_us = (double)N * (double)K * nw / 6.2e6;
+    double best_us = 7.0 + std::max(1.25 * hbm_us, (double)(div_up(tiles, kPairs) * div_up(K, I8_KC)) * 0.36);
     for (int nt = 16; nt <= 128; nt *= 2) {
         if (nt > 16 && nt >= 2 * M) break;
         const int64_t t = div_up(M, nt) * div_up(N, 128), cols = std::min<int64_t>(M, nt) * nw;
         if (t > 16 * kSMs) continue;   // far into k_i8_tile's range
-        const I8Plan p = make_plan(t, chunks, cols, kSMs, 0.28 * nw, true);
-        const double stage_us = std::max(0.21, 0.0115 * (16 * nw + nt / 8));
+        const double kb = (double)(u * (16 * nw + nt / 8));
+        const double stage_us = nw == 1 ? std::max(0.30, 0.0078 * kb) : 0.0115 * kb;
+        const I8Plan p = make_plan(t, chunks, cols, kSMs, stage_us, true);
         const double each = (double)p.full * chunks +
                             (p.rem == 0 ? 0.0 : p.cuts == 0 ? (double)p.rem * chunks / kSMs : (double)chunks / p.cuts);
-        const double us = std::max(hbm_us, each * stage_us) + 4.0 + 0.02 * cols +
+        const double read_us = hbm_us * (1.0 + 0.5 * (double)(div_up(M, nt) - 1));
+        const double us = std::max(read_us, each * stage_us) + 4.0 + 0.02 * cols +
                           (p.cuts == 1 ? 0.0 : p.cluster ? cluster_fix_us(cols) : 5.0 + 0.08 * cols);
         if (us < best_us) {
             best_us = us;
