@@ -15,7 +15,17 @@
 //   code = bf16(0x4300 | (b & 0x7F)) - bf16(0x4300 | (b & 0x80))
 // (128 + low bits, less 128 or 256: exact).  Lanes are laid out so that both
 // the 4-byte reads and the 16-byte writes use all banks.  A weight byte
-// crosses HBM once for NT tokens and is never stored wider.
+// crosses HBM once for NT tokens and is never stored wider.  g costs its terms
+// up to 2^-8 of their size (half a step of bf16): errors of dx come to 0.0023 of
+// its norm, where rounding the result alone gives 0.0017.
+//
+// Bound by shared memory: for 64 channels x 256 tokens each SM takes 8 KB of
+// codes and 16 KB of tokens in, reads the codes, writes and reads 16 KB of
+// operand and reads 16 KB of tokens, 80 KB or 640 cycles where the tensor cores
+// need 512; 32 tokens take 104 KB for 16 KB of codes, 830 cycles where HBM needs
+// 700.  Measured: 2048 tokens, 4096 x 14336 175 us, 1.38 PFLOP/s (tensor pipes
+// 73% active, clocks down to 1.6 GHz by power); 16 tokens, 8192 x 28672 56 us,
+// 4.2 TB/s.
 //
 // Work is handed to the pairs as in k_i8_stream; the fp32 partial sums of a
 // cut tile are added in the order of the pieces by the last contributor,
