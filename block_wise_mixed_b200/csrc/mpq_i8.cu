@@ -172,9 +172,6 @@ inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;
 }
 
-// Tokens per tile of the gradient kernel.
-inline int dx_nt(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
-
 // Pieces that a tile of `chunks` stages may be cut into: a stage costs about as
 // long as the last contributor takes to add 14 columns of one more partial sum,
 // so n pieces cost chunks / n + n cols / 14, least at n = sqrt(14 chunks / cols).
@@ -184,16 +181,18 @@ inline int64_t max_cuts(int64_t chunks, int64_t cols) {
 // What it costs to add up a tile between the CTAs of a cluster.
 inline double cluster_fix_us(int64_t cols) { return 2.0 + 0.02 * (double)cols; }
 
-// chunk_us: a stage's time.  Cuts, or equal runs, only where the time they take
-// off is worth more than a fix-up, about 5 us and 0.08 us a column (measured:
-// 16-token gradient of 8192 x 28672, 112 tiles on 74 pairs: 55 us in runs, 62
-// whole; one token through 14336 x 4096: 16.8 us in runs, 13.6 whole).
-I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, double chunk_us, bool clusters) {
+// chunk_us: a stage's time; fix_us: what adding up a tile that is cut through
+// global memory costs.  Cuts, or equal runs, only where the time they take off
+// is worth more (measured: 16-token gradient of 8192 x 28672, 112 tiles on 74
+// pairs: 55 us in runs, 62 whole; one token through 14336 x 4096: 16.8 us in runs,
+// 13.6 whole).
+I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, double chunk_us, double fix_us,
+                 bool clusters) {
     I8Plan p{};
     p.full = (int)(tiles / workers);
     p.rem = (int)(tiles % workers);
     p.cuts = 1;
-    const double fix_us = 5.0 + 0.08 * (double)cols, tile_us = (double)chunks * chunk_us;
+    const double tile_us = (double)chunks * chunk_us;
     if (clusters && p.full == 0 && p.rem > 0 && workers / p.rem >= 2) {   // (no tiles: an empty batch)
         // All clusters at once: the occupancy query gives 74, 45, 33, 26, 22, 15
         // and 15 clusters of 2 to 8 CTAs; a few less here, as a second wave
@@ -215,6 +214,12 @@ I8Plan make_plan(int64_t tiles, int64_t chunks, int64_t cols, int workers, doubl
     }
     p.workers = p.full || p.cuts == 0 ? workers : p.rem * p.cuts;
     return p;
+}
+
+// Stages of the worker that has most.
+inline double stages_each(const I8Plan& p, int64_t chunks, int workers) {
+    return (double)p.full * chunks +
+           (p.rem == 0 ? 0.0 : p.cuts == 0 ? (double)p.rem * chunks / workers : (double)chunks / p.cuts);
 }
 
 // Which kernel makes a product, and how.
@@ -245,12 +250,12 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
         if (t > 16 * kSMs) continue;   // far into k_i8_tile's range
         const double kb = (double)(u * (16 * nw + nt / 8));
         const double stage_us = nw == 1 ? std::max(0.30, 0.0078 * kb) : 0.0115 * kb;
-        const I8Plan p = make_plan(t, chunks, cols, kSMs, stage_us, true);
-        const double each = (double)p.full * chunks +
-                            (p.rem == 0 ? 0.0 : p.cuts == 0 ? (double)p.rem * chunks / kSMs : (double)chunks / p.cuts);
+        const double fix_us = 5.0 + 0.08 * cols;
+        const I8Plan p = make_plan(t, chunks, cols, kSMs, stage_us, fix_us, true);
+        const double each = stages_each(p, chunks, kSMs);
         const double read_us = hbm_us * (1.0 + 0.5 * (double)(div_up(M, nt) - 1));
         const double us = std::max(read_us, each * stage_us) + 4.0 + 0.02 * cols +
-                          (p.cuts == 1 ? 0.0 : p.cluster ? cluster_fix_us(cols) : 5.0 + 0.08 * cols);
+                          (p.cuts == 1 ? 0.0 : p.cluster ? cluster_fix_us(cols) : fix_us);
         if (us < best_us) {
             best_us = us;
             best = {nt, p};
@@ -258,9 +263,32 @@ ProductPlan product_plan(int64_t M, int64_t N, int64_t K, int nw) {
     }
     return best;
 }
-inline I8Plan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
-    const int nt = dx_nt(M), u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
-    return make_plan(div_up(M, nt) * div_up(K, 256), div_up(N, I8X_NC * u) * nw, std::min<int64_t>(M, nt), kPairs, 0.3, false);
+
+// Tokens per tile of the gradient kernel, and its work.  As above: a stage takes
+// 0.42, 0.45 or 0.55 us (two 64-channel blocks, 32, 64 or 128 tokens) or 0.34
+// (one block, 256 tokens); adding up a cut tile 5 + 0.045 a column (256 tokens,
+// 4096 x 4096: 29 us in tiles of 256 cut in four, 24 in whole tiles of 64).
+struct DxPlan {
+    int nt;
+    I8Plan work;
+};
+DxPlan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
+    static const double kStage[4] = {0.42, 0.45, 0.55, 0.34};
+    DxPlan best{};
+    double best_us = 0.0;
+    for (int i = 0; i < 4; ++i) {
+        const int nt = 32 << i, u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
+        if (i > 0 && nt >= 2 * M) break;
+        const int64_t chunks = div_up(N, I8X_NC * u) * nw, cols = std::min<int64_t>(M, nt);
+        const double fix_us = 5.0 + 0.045 * cols;
+        const I8Plan p = make_plan(div_up(M, nt) * div_up(K, 256), chunks, cols, kPairs, kStage[i], fix_us, false);
+        const double us = stages_each(p, chunks, kPairs) * kStage[i] + 0.02 * cols + (p.cuts == 1 ? 0.0 : fix_us);
+        if (i == 0 || us < best_us) {
+            best_us = us;
+            best = {nt, p};
+        }
+    }
+    return best;
 }
 inline int64_t plan_slots(const I8Plan& p) {
     return p.cuts == 0 ? 2 * p.workers : p.cuts == 1 || p.cluster ? 0 : (int64_t)p.rem * p.cuts;
@@ -272,7 +300,8 @@ inline size_t product_slots(int64_t M, int64_t N, int64_t K, int nw) {
     return p.nt == 0 ? 0 : (size_t)plan_slots(p.work) * nw * p.nt * 128 * 4;
 }
 inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
-    return (size_t)plan_slots(dx_plan(M, N, K, nw)) * 2 * dx_nt(M) * 128 * 4;
+    const DxPlan p = dx_plan(M, N, K, nw);
+    return (size_t)plan_slots(p.work) * 2 * p.nt * 128 * 4;
 }
 
 inline int64_t grad_ld(int64_t n) { return div_up(n, 64) * 64; }
@@ -411,13 +440,12 @@ mpq_status product_run(const mpq_i8* x, const mpq_i8* const* w, I8Product& p, co
 
 template <int NT>
 mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, I8DxParams& p,
-                  void* stream) {
+                  const I8Plan& plan, void* stream) {
     CUtensorMap w0, w1, g0, g1;
     if (!make_map(&w0, w[0], I8DxCfg<NT>::U * I8X_NC, false) || !make_map(&w1, w[nw - 1], I8DxCfg<NT>::U * I8X_NC, false) ||
         !make_map(&g0, g, true, p.M, p.N, ldg * 2, NT / 2, true) ||
         !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
-    const I8Plan plan = dx_plan(p.M, p.N, p.K, nw);
     return launch_big<k_i8_dx<NT>>(0, dim3((unsigned)(2 * plan.workers)), I8DxCfg<NT>::WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
                                    stream, w0, w1, g0, g1, p, plan);
 }
@@ -434,11 +462,12 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
     p.err = ws.err;
     p.counters = ws.counters;
     p.slots = static_cast<float*>(ws.slots);
-    switch (dx_nt(M)) {
-        case 32: return dx_run<32>(w, nw, g, ldg, up_off, p, stream);
-        case 64: return dx_run<64>(w, nw, g, ldg, up_off, p, stream);
-        case 128: return dx_run<128>(w, nw, g, ldg, up_off, p, stream);
-        default: return dx_run<256>(w, nw, g, ldg, up_off, p, stream);
+    const DxPlan plan = dx_plan(M, p.N, p.K, nw);
+    switch (plan.nt) {
+        case 32: return dx_run<32>(w, nw, g, ldg, up_off, p, plan.work, stream);
+        case 64: return dx_run<64>(w, nw, g, ldg, up_off, p, plan.work, stream);
+        case 128: return dx_run<128>(w, nw, g, ldg, up_off, p, plan.work, stream);
+        default: return dx_run<256>(w, nw, g, ldg, up_off, p, plan.work, stream);
     }
 }
 
