@@ -15,9 +15,15 @@
 //   code = bf16(0x4300 | (b & 0x7F)) - bf16(0x4300 | (b & 0x80))
 // (128 + low bits, less 128 or 256: exact).  Lanes are laid out so that both
 // the 4-byte reads and the 16-byte writes use all banks.  A weight byte
-// crosses HBM once for NT tokens and is never stored wider.  g costs its terms
-// up to 2^-8 of their size (half a step of bf16): errors of dx come to 0.0023 of
-// its norm, where rounding the result alone gives 0.0017.
+// crosses HBM once for NT tokens and is never stored wider.
+// A bf16 g costs its terms up to 2^-8 of their size (half a step).  Over many
+// tokens that brings the error of dx to 0.0023 of its norm, where rounding the
+// result alone gives 0.0017; for few tokens and columns there is little to
+// average over, and it reached 0.006.  Up to 16 tokens, where the instruction has
+// twice the columns anyway, g therefore comes in two bf16 parts (16 bits), as
+// twice the tokens: the first CTA of a pair fetches the first parts, the second
+// the second, and the epilogue adds their columns (64 tokens so: 62 -> 74 us for
+// 8192 x 28672).
 //
 // Bound by shared memory: for 64 channels x 256 tokens each SM takes 8 KB of
 // codes and 16 KB of tokens in, reads the codes, writes and reads 16 KB of
@@ -83,6 +89,7 @@ struct I8DxParams {
     uint16_t* dx;
     int64_t lddx;
     int M, N, K, nw;
+    int split;     // (NT = 32) g in two parts: rows M .. 2 M - 1 hold the second
     uint32_t* err;
     uint32_t* counters;
     float* slots;
@@ -112,7 +119,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     const uint32_t rank = cluster_rank();
 
     const int NB = (p.N + U * I8X_NC - 1) / (U * I8X_NC), C = NB * p.nw;
-    const int64_t TM = (p.M + NT - 1) / NT;
+    const bool split = NT == 32 && p.split;
+    const int tok = split ? NT / 2 : NT;     // tokens of a tile
+    const int64_t TM = (p.M + tok - 1) / tok;
     const int pair = blockIdx.x >> 1;
     const I8Work work(plan, pair, C);
     const int n_segs = work.segs;
@@ -185,7 +194,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         bool ok = !kI8WaitTest;
         for (int j = 0; j < n_segs && ok; ++j) {
             const I8Seg g = work.seg(j);
-            const int m0 = (int)(g.tile % TM) * NT + (int)rank * (NT / 2);
+            const int m0 = (int)(g.tile % TM) * tok + (int)rank * (split ? p.M : NT / 2);
             for (int c = g.k0; c < g.k1; ++c) {
                 const bool second = c >= NB;
                 ok = i8_wait_warp(&sm.empty[s], ph);
@@ -257,12 +266,23 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 break;
             }
             i8_fence_after();
-            const int64_t k = (g.tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (g.tile % TM) * NT;
-            const int mc = (int)min((int64_t)NT, p.M - m0);
+            const int64_t k = (g.tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (g.tile % TM) * tok;
+            const int mc = (int)min((int64_t)tok, p.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NT);
             const int c0 = g.c0, c1 = g.c1;
             auto slot_of = [&](int c) {
                 return p.slots + ((size_t)(work.slot(c, c0) * 2 + rank) * NT) * 128 + quad * 32 + lane;
+            };
+            // This CTA's sums of columns c .. c + 31 (both parts).
+            auto own_sums = [&](int c, float (&v)[32]) {
+                uint32_t t[32];
+                i8_tmem_ld32(taddr + (uint32_t)c, t);
+                i8_tmem_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(t[i]);
+                if (split)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += v[16 + i];   // columns of the second parts
             };
             // A cut tile: when all others have arrived already, this one only
             // adds; else it leaves its part and counts itself in.
@@ -275,12 +295,11 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 if (__shfl_sync(0xffffffffu, seen, 0) != others) {
                     float* slot = slot_of(pair);
                     for (int c = 32 * half; c < mc; c += 8 * EPI) {
-                        uint32_t r[32];
-                        i8_tmem_ld32(taddr + (uint32_t)c, r);
-                        i8_tmem_wait();
+                        float r[32];
+                        own_sums(c, r);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c + i < mc) slot[(c + i) * 128] = __uint_as_float(r[i]);
+                            if (c + i < mc) slot[(c + i) * 128] = r[i];
                     }
                     __threadfence();
                     __syncwarp();
@@ -298,18 +317,17 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     for (int o = c0; o <= c1; ++o) {   // in the order of the pieces
-                        uint32_t t[32];
+                        float t[32];
                         if (o == pair) {
-                            i8_tmem_ld32(taddr + (uint32_t)c, t);
-                            i8_tmem_wait();
+                            own_sums(c, t);
                         } else {
                             const float* slot = slot_of(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                t[i] = c + i < mc ? __float_as_uint(__ldcg(slot + (c + i) * 128)) : 0u;
+                                t[i] = c + i < mc ? __ldcg(slot + (c + i) * 128) : 0.f;
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(t[i]);
+                        for (int i = 0; i < 32; ++i) v[i] += t[i];
                     }
                     if (k < p.K) {
                         uint16_t* dx = p.dx + (m0 + c) * p.lddx + k;
@@ -413,12 +431,12 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 }
 
 // ---------------------------------------------------------------------------
-// g = dy * scale of its channel, rounded to bf16 (the operand above).
+// g = dy * scale of its channel in bf16, in one part or two (the operand above).
 // ---------------------------------------------------------------------------
 // A thread keeps its columns' scales and goes down the rows.
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64_t lddy, const float* s, uint16_t* g,
-                                                       int64_t ldg, int M, int N) {
+                                                       int64_t ldg, int64_t lo_off, int M, int N) {
     constexpr int PER = VEC ? 8 : 2;
     const int n = (blockIdx.x * 256 + threadIdx.x) * PER;   // g's rows are padded to 64
     pdl_wait();
@@ -452,12 +470,21 @@ __global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (m0 + i >= M) break;
-            uint32_t o[PER / 2];
+            uint32_t o[PER / 2], l[PER / 2];
 #pragma unroll
-            for (int j = 0; j < PER / 2; ++j) o[j] = pack_bf16(bf16_lo(w[i][j]) * sc[2 * j], bf16_hi(w[i][j]) * sc[2 * j + 1]);
-            uint32_t* out = reinterpret_cast<uint32_t*>(g + (int64_t)(m0 + i) * ldg + n);
-            if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[PER > 2 ? 1 : 0], o[PER > 4 ? 2 : 0], o[PER > 6 ? 3 : 0]);
-            else *out = o[0];
+            for (int j = 0; j < PER / 2; ++j) {
+                const float a = bf16_lo(w[i][j]) * sc[2 * j], b = bf16_hi(w[i][j]) * sc[2 * j + 1];
+                o[j] = pack_bf16(a, b);
+                l[j] = bf16_rest(a, b, o[j]);
+            }
+            auto put = [&](uint16_t* at, const uint32_t (&v)[PER / 2]) {
+                uint32_t* out = reinterpret_cast<uint32_t*>(at);
+                if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[PER > 2 ? 1 : 0], v[PER > 4 ? 2 : 0], v[PER > 6 ? 3 : 0]);
+                else *out = v[0];
+            };
+            uint16_t* at = g + (int64_t)(m0 + i) * ldg + n;
+            put(at, o);
+            if (lo_off) put(at + lo_off, l);   // the second parts
         }
     }
 }

@@ -54,6 +54,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return r;
 }
 
+// What rounding a and b to the pair h left, rounded to bf16 again.
+__device__ __forceinline__ uint32_t bf16_rest(float a, float b, uint32_t h) {
+    return pack_bf16(a - bf16_lo(h), b - bf16_hi(h));
+}
+
 template <bool BF16>
 struct I8Elem;
 template <>

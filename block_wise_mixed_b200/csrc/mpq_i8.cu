@@ -272,16 +272,22 @@ struct DxPlan {
     int nt;
     I8Plan work;
 };
+// Gradients in two bf16 parts up to here (see k_i8_dx.cuh): tiles of 32 columns
+// then hold 16 tokens.
+constexpr int kDxSplitM = 16;
+inline int grad_parts(int64_t M) { return M <= kDxSplitM ? 2 : 1; }
+
 DxPlan dx_plan(int64_t M, int64_t N, int64_t K, int nw) {
     static const double kStage[4] = {0.42, 0.45, 0.55, 0.34};
     DxPlan best{};
     double best_us = 0.0;
     for (int i = 0; i < 4; ++i) {
         const int nt = 32 << i, u = nt == 256 ? I8DxCfg<256>::U : I8DxCfg<32>::U;
-        if (i > 0 && nt >= 2 * M) break;
-        const int64_t chunks = div_up(N, I8X_NC * u) * nw, cols = std::min<int64_t>(M, nt);
+        const int64_t tok = nt / grad_parts(M);
+        if (i > 0 && tok >= 2 * M) break;
+        const int64_t chunks = div_up(N, I8X_NC * u) * nw, cols = std::min<int64_t>(M, tok);
         const double fix_us = 5.0 + 0.045 * cols;
-        const I8Plan p = make_plan(div_up(M, nt) * div_up(K, 256), chunks, cols, kPairs, kStage[i], fix_us, false);
+        const I8Plan p = make_plan(div_up(M, tok) * div_up(K, 256), chunks, cols, kPairs, kStage[i], fix_us, false);
         const double us = stages_each(p, chunks, kPairs) * kStage[i] + 0.02 * cols + (p.cuts == 1 ? 0.0 : fix_us);
         if (i == 0 || us < best_us) {
             best_us = us;
@@ -332,7 +338,7 @@ I8Ws ws_product(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
 // nw matrices: the product's slots (gated) and the gradient's share their place.
 I8Ws ws_backward(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
     const size_t ps = nw == 2 ? product_slots(M, N, K, 2) : 0;
-    return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * (size_t)grad_ld(N) * 2 * (size_t)nw);
+    return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * grad_parts(M) * (size_t)grad_ld(N) * 2 * (size_t)nw);
 }
 
 // x and the weights of a product: common columns, at least one channel.
@@ -443,8 +449,8 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
                   const I8Plan& plan, void* stream) {
     CUtensorMap w0, w1, g0, g1;
     if (!make_map(&w0, w[0], I8DxCfg<NT>::U * I8X_NC, false) || !make_map(&w1, w[nw - 1], I8DxCfg<NT>::U * I8X_NC, false) ||
-        !make_map(&g0, g, true, p.M, p.N, ldg * 2, NT / 2, true) ||
-        !make_map(&g1, g + (nw - 1) * up_off, true, p.M, p.N, ldg * 2, NT / 2, true))
+        !make_map(&g0, g, true, (int64_t)p.M * grad_parts(p.M), p.N, ldg * 2, NT / 2, true) ||
+        !make_map(&g1, g + (nw - 1) * up_off, true, (int64_t)p.M * grad_parts(p.M), p.N, ldg * 2, NT / 2, true))
         return MPQ_ERR_CUDA;
     return launch_big<k_i8_dx<NT>>(0, dim3((unsigned)(2 * plan.workers)), I8DxCfg<NT>::WARPS * 32, sizeof(I8DxSmem<NT>) + 1024,
                                    stream, w0, w1, g0, g1, p, plan);
@@ -459,6 +465,7 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
     p.N = w[0]->rows;
     p.K = w[0]->cols;
     p.nw = nw;
+    p.split = grad_parts(M) == 2;
     p.err = ws.err;
     p.counters = ws.counters;
     p.slots = static_cast<float*>(ws.slots);
@@ -541,8 +548,9 @@ mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M
     const int64_t gx = div_up(w->rows, 256 * (vec ? 8 : 2));
     const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(div_up(M, 4), kSMs * 8 / gx)));
     const uint16_t* dy = static_cast<const uint16_t*>(dy_dev);
-    st = vec ? launch(k_i8_scale_grad<true>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows)
-             : launch(k_i8_scale_grad<false>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, M, w->rows);
+    const int64_t lo_off = grad_parts(M) == 2 ? (int64_t)M * ldg : 0;
+    st = vec ? launch(k_i8_scale_grad<true>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, lo_off, M, w->rows)
+             : launch(k_i8_scale_grad<false>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, lo_off, M, w->rows);
     if (st != MPQ_OK) return st;
     return dx_run(&w, 1, k.grads, ldg, 0, M, dx_dev, lddx, k, stream);
 }
@@ -572,6 +580,7 @@ mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mp
     p.g = k.grads;
     p.up_off = grad_ld(F);
     p.ldg = 2 * p.up_off;
+    p.lo_off = grad_parts(x->rows) == 2 ? (int64_t)x->rows * p.ldg : 0;
     st = act == MPQ_ACT_SILU ? product_run<2, MPQ_ACT_SILU>(x, wl, p, k, stream)
                              : product_run<2, MPQ_ACT_GELU_TANH>(x, wl, p, k, stream);
     if (st != MPQ_OK) return st;

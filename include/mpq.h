@@ -443,8 +443,9 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
 /* Backward passes with respect to the activations; codes and scales are
  * constants (the quantizer's gradient is taken as one).  Gradients are bf16
  * in and out and accumulated in fp32; a gradient that enters a product is
- * rounded to bf16 once, after its channel's scale is applied, and the codes
- * are exact in bf16.
+ * rounded to bf16 once, after its channel's scale is applied (for up to 16
+ * tokens it is carried in two bf16 parts, 16 bits), and the codes are exact in
+ * bf16.
  *
  * mpq_i8_linear_backward:  dx[m][k] = sum_n (dy[m][n] w.scales[n]) w.codes[n][k]
  *   dy: M x N (element (m, n) at m * lddy + n), dx: M x K (lddx).
