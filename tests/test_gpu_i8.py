@@ -402,6 +402,19 @@ def test_gated_backward(mpq, M, F, K, act):
     assert st == 0 and torch.equal(dx2, dx)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1350, 25), (2, 1024, 64), (4, 5000, 3), (16, 4096, 300), (1, 8192, 4096), (7, 100, 7)])
+def test_few_tokens_carry_two_parts(mpq, M, N, K):
+    """Up to 16 tokens the scaled gradient is a sum of two bf16 parts, so it is
+    off by at most half a step of the second, 2^-16 of its size; what is left is
+    the result's own rounding and the fp32 sums."""
+    import torch
+    w = rand_i8(mpq, N, K, 5, 1e-3)
+    dy = (torch.randn(M, N, generator=gen(6), device="cuda") * 0.1).to(torch.bfloat16)
+    want = dy.double() @ hat(w)
+    mag = dy.double().abs() @ hat(w).abs()
+    assert_close(mpq.i8_linear_backward(w, dy), want, (B16 * B16 + u + 2 * N * u) * mag + B16 * want.abs())
+
+
 def test_gradients_against_differences(mpq):
     """dx along random directions against central differences of the block in
     64 bits (x_hat is what the codes stand for)."""
