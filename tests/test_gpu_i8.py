@@ -458,6 +458,31 @@ def test_nonfinite_gradients_stay_in_their_rows(mpq):
     assert (~torch.isfinite(dxl).all(1)).nonzero().flatten().tolist() == [3, 135]
 
 
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 140])
+def test_infinite_gradients_keep_their_sign(mpq, M):
+    """inf times a code is an infinity of the code's sign (NaN for a code of 0),
+    for few tokens, whose gradients go in two parts, as for many."""
+    import torch
+    N, K = 200, 150
+    w = rand_i8(mpq, N, K, 2, 0.01)
+    w.codes[7, 5] = 0
+    dy = torch.ones(M, N, device="cuda", dtype=torch.bfloat16)
+    dy[0, 7] = float("inf")
+    dy[M - 1, 100] = float("-inf")
+    want = (dy.double() * w.scales.double()) @ w.codes.double()
+    dx = mpq.i8_linear_backward(w, dy)
+    bad = ~torch.isfinite(want)
+    assert int(bad.sum()) >= K and torch.equal(~torch.isfinite(dx), bad)
+    assert torch.equal(dx.double().nan_to_num(0.0, 1.0, -1.0)[bad], want.nan_to_num(0.0, 1.0, -1.0)[bad])
+    # and through the gated block
+    x, wg = rand_i8(mpq, M, K, 3, 0.01), rand_i8(mpq, N, K, 4, 0.01)
+    dx, d_gate, d_up = mpq.i8_gated_backward(x, wg, w, dy)
+    want = (d_gate.double() * wg.scales.double()) @ wg.codes.double() + (d_up.double() * w.scales.double()) @ w.codes.double()
+    bad = ~torch.isfinite(want)
+    assert int(bad.sum()) >= K and torch.equal(~torch.isfinite(dx), bad)
+    assert torch.equal(dx.double().nan_to_num(0.0, 1.0, -1.0)[bad], want.nan_to_num(0.0, 1.0, -1.0)[bad])
+
+
 # ------------------------- a block, end to end --------------------------------
 def test_feed_forward_block(mpq):
     """quantize -> gated -> quantize -> linear, each step checked against its
