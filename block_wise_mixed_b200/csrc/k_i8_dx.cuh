@@ -118,10 +118,10 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
 
-    const int NB = (p.N + U * I8X_NC - 1) / (U * I8X_NC), C = NB * p.nw;
+    const int NB = (p.N - 1) / (U * I8X_NC) + 1, C = NB * p.nw;   // (N up to 2^31 - 1)
     const bool split = NT == 32 && p.split;
     const int tok = split ? NT / 2 : NT;     // tokens of a tile
-    const int64_t TM = (p.M + tok - 1) / tok;
+    const int64_t TM = (p.M - 1) / tok + 1;
     const int pair = blockIdx.x >> 1;
     const I8Work work(plan, pair, C);
     const int n_segs = work.segs;
@@ -445,15 +445,15 @@ __global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64
     float sc[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) sc[j] = n + j < N ? s[n + j] : 0.f;
-    const bool whole = n + PER <= N;
-    for (int m0 = blockIdx.y * 4; m0 < M; m0 += gridDim.y * 4) {
+    const bool whole = N - n >= PER;
+    for (int64_t m0 = blockIdx.y * 4; m0 < M; m0 += gridDim.y * 4) {
         uint32_t w[4][PER / 2];   // four rows' gradients in flight
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int j = 0; j < PER / 2; ++j) w[i][j] = 0u;
             if (m0 + i < M) {
-                const uint16_t* d = dy + (int64_t)(m0 + i) * lddy + n;
+                const uint16_t* d = dy + (m0 + i) * lddy + n;
                 if (VEC && whole) {
                     const uint4 u = *reinterpret_cast<const uint4*>(d);
                     w[i][0] = u.x;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64
                 if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[PER > 2 ? 1 : 0], v[PER > 4 ? 2 : 0], v[PER > 6 ? 3 : 0]);
                 else *out = v[0];
             };
-            uint16_t* at = g + (int64_t)(m0 + i) * ldg + n;
+            uint16_t* at = g + (m0 + i) * ldg + n;
             put(at, o);
             if (lo_off) put(at + lo_off, l);   // the second parts
         }

@@ -62,7 +62,7 @@ k_i8_tile(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUte
     const uint32_t rank = cluster_rank();
 
     const int KB = (p.K + I8_KC - 1) / I8_KC;
-    const int64_t T = (p.N + BN - 1) / BN, TM = (p.M + 255) / 256, tiles = T * TM;
+    const int64_t T = (p.N - 1) / BN + 1, TM = (p.M - 1) / 256 + 1, tiles = T * TM;   // (sizes up to 2^31 - 1)
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (tid == 0) {

@@ -718,3 +718,40 @@ def test_offsets_beyond_32_bits(mpq):
     for m in (0, 65535, 65536, M - 1):
         want = product64(mpq.i8_matrix(x.codes[m:m + 1], x.scales[m:m + 1]), w)
         assert_close(y[m:m + 1], want, (4 * u + B16) * want.abs())
+
+
+def test_largest_row_counts(mpq):
+    """2^31 - 1 channels and 2^31 - 1 tokens: counts of tiles and last columns."""
+    import torch
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of free device memory")
+    R, K, E = 2 ** 31 - 1, 16, 300
+    codes = torch.zeros((R, K), dtype=torch.int8, device="cuda")
+    for i, part in enumerate((codes[:E], codes[-E:])):
+        part.copy_(torch.randint(-127, 128, (E, K), generator=gen(i), device="cuda", dtype=torch.int8))
+    big = mpq.i8_matrix(codes, torch.full((R,), 0.5, device="cuda"))
+    ends = mpq.i8_matrix(torch.cat([codes[:E], codes[-E:]]), torch.full((2 * E,), 0.5, device="cuda"))
+    one = rand_i8(mpq, 1, K, 2)
+    want = product64(one, ends)
+
+    def check(y, want, tol):   # a row of R values: zero but for its ends
+        assert_close(torch.cat([y[:E], y[-E:]])[None].double(), want, tol)
+        for i in range(E, R - E, 1 << 28):
+            assert not bool(y[i:min(i + (1 << 28), R - E)].any())
+
+    check(mpq.i8_linear(one, big, ydtype=mpq.Y_BF16)[0], want, (4 * u + B16) * want.abs())
+    check(mpq.i8_linear(big, one, ydtype=mpq.Y_BF16)[:, 0], want, (4 * u + B16) * want.abs())
+    h = mpq.i8_gated(one, big, big)[0]
+    sig = torch.sigmoid(want)
+    rel = (20 + 15 * want.abs().clamp_max(110)) * u + B16
+    check(h, want * want * sig, rel * want * want * sig + 1e-30 * (1 + want.abs()))
+    del h
+    dy = torch.zeros((1, R), dtype=torch.bfloat16, device="cuda")
+    for i, part in enumerate((dy[:, :E], dy[:, -E:])):
+        part.copy_(torch.randn(1, E, generator=gen(5 + i), device="cuda"))
+    dx = mpq.i8_linear_backward(big, dy)
+    d = torch.cat([dy[:, :E], dy[:, -E:]], 1).double()
+    want = d @ hat(ends)
+    # (terms that are zero add without a rounding)
+    assert_close(dx, want, (B16 * B16 + u + 4 * E * u) * (d.abs() @ hat(ends).abs()) + B16 * want.abs())
