@@ -150,7 +150,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m, uint32_t* red, int t) 
 
 // A row as the 16-byte blocks that cover it: elements off .. end - 1 of the
 // array at x.  Without SHIFT rows are whole blocks; with it the first and the
-// last block may hold elements of the gap or the row beside, which `mask`
+// last block may hold elements of the gap or the rows beside, which `mask`
 // takes out (before the array's start and behind its end nothing is read).
 template <bool BF16, bool SHIFT>
 struct I8Row {
@@ -158,15 +158,16 @@ struct I8Row {
     using T = typename E::T;
     const T* x;
     int off, end, blocks;
-    bool edge0, edge1;   // the array's first row starts, its last row ends, inside a block
+    bool edge0, edge1;   // the first block starts before the array, the last one ends behind it
     __device__ __forceinline__ I8Row(const I8RowsParams& p, int64_t row) {
         x = static_cast<const T*>(p.x) + row * p.ldx;
         off = SHIFT ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0;
         x -= off;
         end = off + p.cols;
         blocks = row < p.rows ? (end + E::PER - 1) / E::PER : 0;
-        edge0 = SHIFT && row == 0 && off != 0;
-        edge1 = SHIFT && row == p.rows - 1 && end % E::PER != 0;
+        // (of few columns, several rows lie in the array's first or last block)
+        edge0 = SHIFT && row * p.ldx < off;
+        edge1 = SHIFT && (p.rows - 1 - row) * p.ldx + end < (int64_t)blocks * E::PER;
     }
     __device__ __forceinline__ uint4 load(int b) const {
         if (b >= blocks) return make_uint4(0u, 0u, 0u, 0u);

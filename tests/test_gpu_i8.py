@@ -137,6 +137,23 @@ def test_quantize_codes_exact(mpq, rows, cols, dtype):
             assert torch.equal(out, v.to(odt)) and guards_ok(buf, rows, cols)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1, 2, 3, 5, 7, 8, 9])
+def test_quantize_narrow_rows(mpq, cols, dtype):
+    """Rows that share their 16-byte blocks with other rows and with what lies
+    before and behind the array (NaN here), from every offset."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for rows in (1, 2, 3, 9, 300):
+        for off in range(9):
+            buf = torch.full((rows * cols + 24,), float("nan"), dtype=dt, device="cuda")
+            x = buf[off:off + rows * cols].view(rows, cols)
+            x.copy_(torch.randn(rows, cols, generator=gen(rows + off), device="cuda"))
+            q = mpq.i8_quantize(x)
+            c64, s64 = quantize64(x)
+            assert torch.equal(q.scales, s64) and torch.equal(q.codes.double(), c64)
+
+
 def test_quantize_rounding_borders(mpq):
     """Quotients on, and a last place beside, every half step; scales over the
     whole range of fp32, subnormal values and zero rows among them."""
