@@ -24,15 +24,15 @@ __device__ __forceinline__ uint64_t i8_smem_desc(uint32_t saddr) {
 }
 
 // Instruction descriptors, both operands K-major: s8 x s8 -> s32, and
-// bf16 x bf16 -> fp32.
+// fp16 x fp16 -> fp32.
 __host__ __device__ constexpr uint32_t i8_idesc(int M, int N) {
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__host__ __device__ constexpr uint32_t bf16_idesc(int M, int N) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+__host__ __device__ constexpr uint32_t f16_idesc(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// KIND 0: i8, 1: f16 (bf16 operands).  PAIR: the two SMs of a cluster.
+// KIND 0: i8, 1: f16.  PAIR: the two SMs of a cluster.
 template <bool PAIR, int KIND>
 __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
 #define MPQ_I8_MMA(GROUP, K)                                                      \

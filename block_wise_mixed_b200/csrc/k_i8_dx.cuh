@@ -3,27 +3,30 @@
 //   dx[m][k] = sum_n g[m][n] w[n][k]     (g = gradient times channel scale)
 //
 // for one weight matrix, or for gate and up as one contraction over both
-// matrices' channels.  g is bf16 and the codes are exact in bf16, so the
-// products run on tcgen05.mma kind::f16 with fp32 sums, 256 k columns x NT
-// tokens over the two SMs of a cluster.
+// matrices' channels.  g is fp16 with a power of two for each token (below) and
+// the codes are exact in fp16, so the products run on tcgen05.mma kind::f16 with
+// fp32 sums, 256 k columns x NT tokens over the two SMs of a cluster, and the
+// epilogue takes the power of two back.
 //
 // The codes lie with k along the rows and the contraction across them; the
-// operand wants the contraction along its rows, in bf16.  Converter warps turn
+// operand wants the contraction along its rows, in fp16.  Converter warps turn
 // each 64 x 128 block of codes (8 KB, by TMA) into the swizzled 128 x 64 operand:
 // a thread takes 8 rows x 4 columns, pairs two rows' bytes of a column with
-// one byte permute, and makes them bf16 with two masks and one subtraction:
-//   code = bf16(0x4300 | (b & 0x7F)) - bf16(0x4300 | (b & 0x80))
-// (128 + low bits, less 128 or 256: exact).  Lanes are laid out so that both
+// one byte permute, and makes them fp16 with one mask and one subtraction:
+//   code = fp16(0x6400 | (b ^ 0x80)) - 1152
+// (1024 + code + 128: exact).  Lanes are laid out so that both
 // the 4-byte reads and the 16-byte writes use all banks.  A weight byte
 // crosses HBM once for NT tokens and is never stored wider.
-// A bf16 g costs its terms up to 2^-8 of their size (half a step).  Over many
-// tokens that brings the error of dx to 0.0023 of its norm, where rounding the
-// result alone gives 0.0017; for few tokens and columns there is little to
-// average over, and it reached 0.006.  Up to 16 tokens, where the instruction has
-// twice the columns anyway, g therefore comes in two bf16 parts (16 bits), as
-// twice the tokens: the first CTA of a pair fetches the first parts, the second
-// the second, and the epilogue adds their columns (64 tokens so: 62 -> 74 us for
-// 8192 x 28672).
+// g in bf16 costs its terms up to 2^-8 of their size (half a step) and brought
+// the error of dx to 0.0023 of its norm, where rounding the result alone gives
+// 0.0017.  fp16 at the same rate costs 2^-11, if its exponents reach: a power of
+// two for each token puts the token's largest |g| into [2^14, 2^15), which leaves
+// 28 powers of two below it with all 11 bits and what is smaller still within
+// 2^-39 of the largest.  So k_i8_grad_rows makes the operand a token at a time
+// (the gated product leaves its scaled gradients in fp32 for it).  Up to 16
+// tokens, where the instruction has twice the columns anyway, g comes in two
+// fp16 parts (22 bits), as twice the tokens: the first CTA of a pair fetches the
+// first parts, the second the second, and the epilogue adds their columns.
 //
 // Bound by shared memory: for 64 channels x 256 tokens each SM takes 8 KB of
 // codes and 16 KB of tokens in, reads the codes, writes and reads 16 KB of
@@ -41,8 +44,6 @@
 // as its own stages allow; warp 1 of the first CTA issues, the EPI warps from 2
 // on finish (lane = k column), the rest convert.  Every wait is bounded.
 #pragma once
-#include <cuda_bf16.h>
-
 #include "k_i8_stream.cuh"
 
 namespace mpq {
@@ -90,18 +91,17 @@ struct I8DxParams {
     int64_t lddx;
     int M, N, K, nw;
     int split;     // (NT = 32) g in two parts: rows M .. 2 M - 1 hold the second
+    const float* unscale;   // one a token
     uint32_t* err;
     uint32_t* counters;
     float* slots;
 };
 
-// Bytes j of two rows' words as a pair of bf16 values.
-__device__ __forceinline__ uint32_t i8_pair_bf16(uint32_t wa, uint32_t wb, int j) {
+// Bytes j of two rows' words as a pair of fp16 values.
+__device__ __forceinline__ uint32_t i8_pair_f16(uint32_t wa, uint32_t wb, int j) {
     const uint32_t t = __byte_perm(wa, wb, (uint32_t)(j | (j << 4) | ((4 + j) << 8) | ((4 + j) << 12)));
-    const uint32_t lo = lop_and_or(t, 0x007F007Fu, 0x43004300u), hi = lop_and_or(t, 0x00800080u, 0x43004300u);
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&hi));
-    return *reinterpret_cast<const uint32_t*>(&d);
+    const uint32_t b = (t & 0x00FF00FFu) ^ 0x64806480u;   // 1152 + code
+    return h2_bits(__hsub2(bits_h2(b), bits_h2(0x64806480u)));
 }
 
 template <int NT>
@@ -219,7 +219,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            constexpr uint32_t idesc = bf16_idesc(256, NT);
+            constexpr uint32_t idesc = f16_idesc(256, NT);
             const bool issuer = elect_one();
             int s = 0, seg = 0;
             uint32_t ph = 0;
@@ -329,6 +329,9 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] += t[i];
                     }
+                    const float us = c + lane < mc ? p.unscale[m0 + c + lane] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, us, i);
                     if (k < p.K) {
                         uint16_t* dx = p.dx + (m0 + c) * p.lddx + k;
                         const int left = mc - c;
@@ -394,8 +397,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<uint4*>(sm.a[s] + b * I8X_A + (at[j] ^ (uint32_t)(64 * h))) =
-                            make_uint4(i8_pair_bf16(in[h][0], in[h][1], j), i8_pair_bf16(in[h][2], in[h][3], j),
-                                       i8_pair_bf16(in[h][4], in[h][5], j), i8_pair_bf16(in[h][6], in[h][7], j));
+                            make_uint4(i8_pair_f16(in[h][0], in[h][1], j), i8_pair_f16(in[h][2], in[h][3], j),
+                                       i8_pair_f16(in[h][4], in[h][5], j), i8_pair_f16(in[h][6], in[h][7], j));
             }
             fence_proxy_async_smem();   // to the tensor cores
             __syncwarp();
@@ -431,61 +434,131 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 }
 
 // ---------------------------------------------------------------------------
-// g = dy * scale of its channel in bf16, in one part or two (the operand above).
+// The gradients as the product's operand: rows of fp16 in one part or two.
 // ---------------------------------------------------------------------------
-// A thread keeps its columns' scales and goes down the rows.
-template <bool VEC>
-__global__ void __launch_bounds__(256) k_i8_scale_grad(const uint16_t* dy, int64_t lddy, const float* s, uint16_t* g,
-                                                       int64_t ldg, int64_t lo_off, int M, int N) {
-    constexpr int PER = VEC ? 8 : 2;
-    const int n = (blockIdx.x * 256 + threadIdx.x) * PER;   // g's rows are padded to 64
+struct I8GradParams {
+    const void* src;       // SRC 0, 1: dy in bf16, M x N; 2: scaled fp32 gradients, laid out as g
+    int64_t ld;
+    const float* s;        // channel scales (SRC 0, 1)
+    uint16_t* g;           // fp16 [M][ldg], the up half (SRC 2) at + up_off
+    int64_t ldg, up_off;
+    int64_t lo_off;        // the second parts, at + lo_off (0: none)
+    float* unscale;        // [M]: what brings a token's sums back
+    int N, cluster;        // channels; blocks of a token
+};
+
+// A block a token, or a cluster of blocks for few tokens: its values times the channels' scales (SRC 2: already done),
+// the largest finite magnitude, and the fp16 parts of the values times the power
+// of two that takes that magnitude into [2^14, 2^15) (2^126 at most, which
+// leaves smaller values exact or with their 11 bits all the same).
+// A thread takes 8 neighbouring columns at a time and keeps its first four such
+// units between the two passes; what is beyond them is read again.
+// SRC 0: rows of dy start at 16-byte blocks.
+// Bound by its bytes where they are many (512 tokens, gate and up of 14336: 59 MB
+// in, 29 out, mostly through L2, and the product's fp32 stores: 16 us of 189) and
+// by latency where they are few (1 to 2 us).
+template <int SRC>
+__global__ void __launch_bounds__(1024) k_i8_grad_rows(I8GradParams p) {
+    constexpr int KEEP = 4;
+    __shared__ uint32_t red[32], top_of;
+    const int64_t m = blockIdx.x / p.cluster;
+    const int first = (int)(blockIdx.x % p.cluster * blockDim.x + threadIdx.x), step = (int)blockDim.x * p.cluster;
+    const int per = (p.N - 1) / 8 + 1, units = SRC == 2 ? 2 * per : per;
+    const bool s_vec = (reinterpret_cast<uintptr_t>(p.s) & 15) == 0;
     pdl_wait();
     pdl_launch_dependents();
-    if (n >= N) return;
-    float sc[PER];
+
+    auto offset = [&](int u) { return SRC == 2 && u >= per ? p.up_off + (int64_t)(u - per) * 8 : (int64_t)u * 8; };
+    auto load = [&](int u, float (&f)[8]) {
+        const int col = (SRC == 2 && u >= per ? u - per : u) * 8;
+        const bool whole = p.N - col >= 8;
+        if (SRC == 2) {
+            const float* x = static_cast<const float*>(p.src) + m * p.ld + offset(u);   // (rows are padded to 64)
+            const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            if (!whole)
 #pragma unroll
-    for (int j = 0; j < PER; ++j) sc[j] = n + j < N ? s[n + j] : 0.f;
-    const bool whole = N - n >= PER;
-    for (int64_t m0 = blockIdx.y * 4; m0 < M; m0 += gridDim.y * 4) {
-        uint32_t w[4][PER / 2];   // four rows' gradients in flight
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < PER / 2; ++j) w[i][j] = 0u;
-            if (m0 + i < M) {
-                const uint16_t* d = dy + (m0 + i) * lddy + n;
-                if (VEC && whole) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(d);
-                    w[i][0] = u.x;
-                    w[i][PER > 2 ? 1 : 0] = u.y;
-                    w[i][PER > 4 ? 2 : 0] = u.z;
-                    w[i][PER > 6 ? 3 : 0] = u.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j)
-                        if (n + j < N) w[i][j / 2] |= (uint32_t)d[j] << (16 * (j & 1));
-                }
-            }
+                for (int j = 0; j < 8; ++j)
+                    if (col + j >= p.N) f[j] = 0.f;
+            return;
         }
+        const uint16_t* x = static_cast<const uint16_t*>(p.src) + m * p.ld + col;
+        const float* s = p.s + col;
+        if (SRC == 0 && whole) {
+            I8Elem<true>::unpack(*reinterpret_cast<const uint4*>(x), f);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (m0 + i >= M) break;
-            uint32_t o[PER / 2], l[PER / 2];
-#pragma unroll
-            for (int j = 0; j < PER / 2; ++j) {
-                const float a = bf16_lo(w[i][j]) * sc[2 * j], b = bf16_hi(w[i][j]) * sc[2 * j + 1];
-                o[j] = pack_bf16(a, b);
-                l[j] = bf16_rest(a, b, o[j]);
-            }
-            auto put = [&](uint16_t* at, const uint32_t (&v)[PER / 2]) {
-                uint32_t* out = reinterpret_cast<uint32_t*>(at);
-                if (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[PER > 2 ? 1 : 0], v[PER > 4 ? 2 : 0], v[PER > 6 ? 3 : 0]);
-                else *out = v[0];
-            };
-            uint16_t* at = g + (m0 + i) * ldg + n;
-            put(at, o);
-            if (lo_off) put(at + lo_off, l);   // the second parts
+            for (int j = 0; j < 8; ++j) f[j] = whole || j < p.N - col ? I8Elem<true>::get(x[j]) : 0.f;
         }
+        if (s_vec && whole) {
+            const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+            f[0] *= a.x; f[1] *= a.y; f[2] *= a.z; f[3] *= a.w;
+            f[4] *= b.x; f[5] *= b.y; f[6] *= b.z; f[7] *= b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (whole || j < p.N - col) f[j] *= s[j];
+        }
+    };
+    uint32_t top = 0;
+    auto fold = [&](const float (&f)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t a = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+            if (a < 0x7F800000u) top = max(top, a);
+        }
+    };
+    float kept[KEEP][8];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (first + i * step < units) load(first + i * step, kept[i]);
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (first + i * step < units) fold(kept[i]);
+    for (int64_t u = (int64_t)first + KEEP * step; u < units; u += step) {
+        float f[8];
+        load((int)u, f);
+        fold(f);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < blockDim.x / 32 ? red[threadIdx.x & 31] : 0u);
+    if (p.cluster > 1) {
+        if (threadIdx.x == 0) top_of = top;
+        cluster_sync();
+        const uint32_t a = smem_u32(&top_of);
+        for (int r = 0; r < p.cluster; ++r) top = max(top, cluster_load(cluster_map(a, (uint32_t)r)));
+        cluster_sync();   // the peers have read it
+    }
+
+    const int e = (int)(top >> 23), k = e == 0 ? 126 : min(126, 141 - e);   // the largest is in [2^(e - 127), 2^(e - 126))
+    const float scale = __uint_as_float((uint32_t)(127 + k) << 23);
+    if (first == 0) p.unscale[m] = __uint_as_float((uint32_t)(127 - k) << 23);
+    auto put = [&](int u, const float (&f)[8]) {
+        uint32_t w[4];
+        uint16_t* g = p.g + m * p.ldg + offset(u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = h2_bits(__floats2half2_rn(f[2 * j] * scale, f[2 * j + 1] * scale));
+        *reinterpret_cast<uint4*>(g) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (!p.lo_off) return;
+        // what that left, rounded again; nothing where it is infinite or NaN (inf - inf would make a NaN of it)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = __low2float(bits_h2(w[j])), y = __high2float(bits_h2(w[j]));
+            w[j] = h2_bits(__floats2half2_rn(fabsf(x) < INFINITY ? f[2 * j] * scale - x : 0.f,
+                                             fabsf(y) < INFINITY ? f[2 * j + 1] * scale - y : 0.f));
+        }
+        *reinterpret_cast<uint4*>(g + p.lo_off) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        if (first + i * step < units) put(first + i * step, kept[i]);
+    for (int64_t u = (int64_t)first + KEEP * step; u < units; u += step) {
+        float f[8];
+        load((int)u, f);
+        put((int)u, f);
     }
 }
 

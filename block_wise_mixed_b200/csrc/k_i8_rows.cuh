@@ -54,13 +54,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return r;
 }
 
-// What rounding a and b to the pair h left, rounded to bf16 again; nothing
-// where that is infinite or NaN (inf - inf would make a NaN of it).
-__device__ __forceinline__ uint32_t bf16_rest(float a, float b, uint32_t h) {
-    const float x = bf16_lo(h), y = bf16_hi(h);
-    return pack_bf16(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f);
-}
-
 template <bool BF16>
 struct I8Elem;
 template <>

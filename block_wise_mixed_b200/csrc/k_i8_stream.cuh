@@ -73,9 +73,8 @@ struct I8Product {
     int64_t lddh;
     uint16_t* d[2];      // d_gate, d_up (or null)
     int64_t ldd;
-    uint16_t* g;         // scaled gradients [M][ldg], the up half at + up_off
+    float* g;            // scaled gradients [M][ldg], the up half at + up_off
     int64_t ldg, up_off;
-    int64_t lo_off;      // second parts of the scaled gradients, at + lo_off (0: none)
     int M, N, K, y_bf16;
     uint32_t* err;
     uint32_t* counters;  // zero between calls
@@ -113,8 +112,9 @@ template <int MODE>
 struct I8Column {
     uint8_t* y;
     const uint16_t* dh;
-    uint16_t *d0, *d1, *g;
-    int64_t ystep, dhstep, dstep, gstep, up_off, lo_off;
+    uint16_t *d0, *d1;
+    float* g;
+    int64_t ystep, dhstep, dstep, gstep, up_off;
     bool bf16;
 
     __device__ __forceinline__ I8Column(const I8Product& p, int64_t m, int64_t n) {
@@ -131,7 +131,6 @@ struct I8Column {
             gstep = p.ldg;
             g = p.g + m * gstep + n;
             up_off = p.up_off;
-            lo_off = p.lo_off;
         }
     }
     __device__ __forceinline__ float next_dh() {
@@ -166,14 +165,8 @@ struct I8Column {
 #pragma unroll
         for (int i = 0; i < N; ++i, g += gstep)
             if (i < left) {
-                const uint32_t h = pack_bf16(o[i].g, o[i].g1);
-                g[0] = (uint16_t)h;
-                g[up_off] = (uint16_t)(h >> 16);
-                if (lo_off) {
-                    const uint32_t l = bf16_rest(o[i].g, o[i].g1, h);
-                    g[lo_off] = (uint16_t)l;
-                    g[lo_off + up_off] = (uint16_t)(l >> 16);
-                }
+                g[0] = o[i].g;
+                g[up_off] = o[i].g1;
             }
     }
 };

@@ -272,7 +272,7 @@ struct DxPlan {
     int nt;
     I8Plan work;
 };
-// Gradients in two bf16 parts up to here (see k_i8_dx.cuh): tiles of 32 columns
+// Gradients in two fp16 parts up to here (see k_i8_dx.cuh): tiles of 32 columns
 // then hold 16 tokens.
 constexpr int kDxSplitM = 16;
 inline int grad_parts(int64_t M) { return M <= kDxSplitM ? 2 : 1; }
@@ -316,29 +316,36 @@ struct I8Ws {
     uint32_t* err;
     uint32_t* counters;
     void* slots;
-    uint16_t* grads;
+    uint16_t* grads;     // the gradient product's fp16 operand
+    float* grads32;      // the gated product's scaled gradients
+    float* unscale;      // one a token
     size_t bytes;
 };
-I8Ws carve(void* ws, size_t slots, size_t grads) {
+I8Ws carve(void* ws, size_t slots, size_t grads, size_t grads32, size_t unscale) {
     uint8_t* b = static_cast<uint8_t*>(ws);
     I8Ws w{};
-    const size_t after = kI8ZeroBytes + round256(slots);
-    w.bytes = after + round256(grads);
+    const size_t after = kI8ZeroBytes + round256(slots), after16 = after + round256(grads),
+                 after32 = after16 + round256(grads32);
+    w.bytes = after32 + round256(unscale);
     if (!b) return w;
     w.err = reinterpret_cast<uint32_t*>(b);
     w.counters = reinterpret_cast<uint32_t*>(b + kErrBytes);
     w.slots = b + kI8ZeroBytes;
     w.grads = reinterpret_cast<uint16_t*>(b + after);
+    w.grads32 = reinterpret_cast<float*>(b + after16);
+    w.unscale = reinterpret_cast<float*>(b + after32);
     return w;
 }
 
 I8Ws ws_product(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
-    return carve(ws, product_slots(M, N, K, nw), 0);
+    return carve(ws, product_slots(M, N, K, nw), 0, 0, 0);
 }
 // nw matrices: the product's slots (gated) and the gradient's share their place.
 I8Ws ws_backward(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
     const size_t ps = nw == 2 ? product_slots(M, N, K, 2) : 0;
-    return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * grad_parts(M) * (size_t)grad_ld(N) * 2 * (size_t)nw);
+    const size_t row = (size_t)grad_ld(N) * (size_t)nw;
+    return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * grad_parts(M) * row * 2,
+                 nw == 2 ? (size_t)M * row * 4 : 0, (size_t)M * 4);
 }
 
 // x and the weights of a product: common columns, at least one channel.
@@ -370,15 +377,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // rows x cols elements, ld bytes a row, boxes of box_rows x 128 bytes; what
 // lies outside reads as zero.
-bool make_map(CUtensorMap* map, const void* ptr, bool bf16, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+bool make_map(CUtensorMap* map, const void* ptr, bool f16, int64_t rows, int64_t cols, int64_t ld, int box_rows,
               bool swizzle) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld};
-    cuuint32_t box[2] = {bf16 ? 64u : 128u, (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {f16 ? 64u : 128u, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1u, 1u};
-    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -456,6 +463,26 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
                                    stream, w0, w1, g0, g1, p, plan);
 }
 
+// The operand of the gradient product from `src` (SRC as in k_i8_grad_rows).  A thread
+// takes one unit of 8 columns while the SMs have threads enough for all, four at
+// most (256 tokens of 4096 channels, whole gradient: 22.9 us, 25.6 with four);
+// more than 1024 threads a token are a cluster (128000 channels).
+template <int SRC>
+mpq_status grad_rows_run(I8GradParams& p, const I8Ws& ws, int64_t M, int64_t N, int64_t ldg, void* stream) {
+    p.g = ws.grads;
+    p.ldg = ldg;
+    p.lo_off = grad_parts(M) == 2 ? M * ldg : 0;
+    p.unscale = ws.unscale;
+    p.N = (int)N;
+    const int64_t units = div_up(N, 8) * (SRC == 2 ? 2 : 1);
+    const int64_t warps = div_up(units, 32 * std::clamp<int64_t>(div_up(M * units, kSMs * 1024), 1, 4));
+    p.cluster = 1;
+    while (p.cluster < 8 && p.cluster * 32 < warps) p.cluster *= 2;
+    const int threads = (int)std::min<int64_t>(1024, div_up(warps, p.cluster) * 32);
+    return launch_cluster(p.cluster > 1 ? p.cluster : 0, k_i8_grad_rows<SRC>, dim3((unsigned)(M * p.cluster)), threads, 0,
+                          stream, p);
+}
+
 mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, int64_t M,
                   void* dx_dev, int64_t lddx, const I8Ws& ws, void* stream) {
     I8DxParams p{};
@@ -466,6 +493,7 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
     p.K = w[0]->cols;
     p.nw = nw;
     p.split = grad_parts(M) == 2;
+    p.unscale = ws.unscale;
     p.err = ws.err;
     p.counters = ws.counters;
     p.slots = static_cast<float*>(ws.slots);
@@ -545,12 +573,11 @@ mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M
     if (st != MPQ_OK) return st;
     const int64_t ldg = grad_ld(w->rows);
     const bool vec = aligned(dy_dev, 16) && (M == 1 || lddy % 8 == 0);
-    const int64_t gx = div_up(w->rows, 256 * (vec ? 8 : 2));
-    const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(div_up(M, 4), kSMs * 8 / gx)));
-    const uint16_t* dy = static_cast<const uint16_t*>(dy_dev);
-    const int64_t lo_off = grad_parts(M) == 2 ? (int64_t)M * ldg : 0;
-    st = vec ? launch(k_i8_scale_grad<true>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, lo_off, M, w->rows)
-             : launch(k_i8_scale_grad<false>, grid, 256, 0, stream, dy, lddy, w->scales, k.grads, ldg, lo_off, M, w->rows);
+    I8GradParams g{};
+    g.src = dy_dev;
+    g.ld = lddy;
+    g.s = w->scales;
+    st = vec ? grad_rows_run<0>(g, k, M, w->rows, ldg, stream) : grad_rows_run<1>(g, k, M, w->rows, ldg, stream);
     if (st != MPQ_OK) return st;
     return dx_run(&w, 1, k.grads, ldg, 0, M, dx_dev, lddx, k, stream);
 }
@@ -577,12 +604,17 @@ mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mp
     p.d[0] = static_cast<uint16_t*>(d_gate_dev);
     p.d[1] = static_cast<uint16_t*>(d_up_dev);
     p.ldd = ldd;
-    p.g = k.grads;
+    p.g = k.grads32;
     p.up_off = grad_ld(F);
     p.ldg = 2 * p.up_off;
-    p.lo_off = grad_parts(x->rows) == 2 ? (int64_t)x->rows * p.ldg : 0;
     st = act == MPQ_ACT_SILU ? product_run<2, MPQ_ACT_SILU>(x, wl, p, k, stream)
                              : product_run<2, MPQ_ACT_GELU_TANH>(x, wl, p, k, stream);
+    if (st != MPQ_OK) return st;
+    I8GradParams g{};
+    g.src = k.grads32;
+    g.ld = p.ldg;
+    g.up_off = p.up_off;
+    st = grad_rows_run<2>(g, k, x->rows, F, p.ldg, stream);
     if (st != MPQ_OK) return st;
     return dx_run(wl, 2, k.grads, p.ldg, p.up_off, x->rows, dx_dev, lddx, k, stream);
 }

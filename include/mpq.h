@@ -443,9 +443,11 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
 /* Backward passes with respect to the activations; codes and scales are
  * constants (the quantizer's gradient is taken as one).  Gradients are bf16
  * in and out and accumulated in fp32; a gradient that enters a product is
- * rounded to bf16 once, after its channel's scale is applied (for up to 16
- * tokens it is carried in two bf16 parts, 16 bits), and the codes are exact in
- * bf16.
+ * rounded once, after its channel's scale is applied, to 11 bits (2^-11 of its
+ * size, or 2^-39 of the token's largest finite one if that is more): fp16 with a
+ * power of two for each token, against codes that are exact in fp16.  For up to
+ * 16 tokens it is carried in two such parts, 22 bits, so the last bits of a
+ * token's dx may depend on how many tokens the call has.
  *
  * mpq_i8_linear_backward:  dx[m][k] = sum_n (dy[m][n] w.scales[n]) w.codes[n][k]
  *   dy: M x N (element (m, n) at m * lddy + n), dx: M x K (lddx).
