@@ -290,6 +290,16 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) k_i8_quantize(I8RowsParams 
     }
 }
 
+// Word w (codes 4 w .. 4 w + 3) of a row of `cols` codes; bytes behind the last
+// column read as zero and are not touched.
+__host__ __device__ __forceinline__ uint32_t i8_codes_word(const int8_t* codes, int w, int cols) {
+    const int left = cols - 4 * w;
+    if (left >= 4) return reinterpret_cast<const uint32_t*>(codes)[w];
+    uint32_t v = 0u;
+    for (int j = 0; j < left; ++j) v |= (uint32_t)(uint8_t)codes[4 * w + j] << (8 * j);
+    return v;
+}
+
 // x = code * scale.  VEC (16-byte aligned rows of x): 16 bytes of x a thread,
 // four times.  Otherwise a warp takes 128 codes as 32 words and deals them
 // out, so that lane l stores elements 32 j + l: whole lines at any alignment,
@@ -309,14 +319,12 @@ __global__ void __launch_bounds__(256) k_i8_dequantize(I8RowsParams p) {
         else reinterpret_cast<float*>(y)[c] = v;
     };
     if (!VEC) {
-        // words beyond the last column lie inside the row's pitch or are not read
         const int lane = threadIdx.x & 31, words = (p.cols + 3) / 4;
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(codes);
         const int per = 8 * 32;   // words of a warp's piece
         for (int w0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * per; w0 < words; w0 += gridDim.y * 8 * per) {
             uint32_t r[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = w0 + 32 * i + lane < words ? w[w0 + 32 * i + lane] : 0u;
+            for (int i = 0; i < 8; ++i) r[i] = i8_codes_word(codes, w0 + 32 * i + lane, p.cols);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll

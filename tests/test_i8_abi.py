@@ -2,6 +2,8 @@
 validation through the C ABI (no call here reaches a launch), workspace sizes
 and the binding's tensor checks."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -173,3 +175,13 @@ def test_binding_refuses(lib):
         B.i8_matrix(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4))
     with pytest.raises(B.MpqError):
         B.i8_linear(x, x)                      # no int8 matrices
+
+
+def test_row_words_end_at_the_last_column(tmp_path):
+    """The host build of the row kernels' fetch of codes (tests/native/i8_words.cu)."""
+    exe = tmp_path / "i8_words"
+    src = os.path.join(os.path.dirname(__file__), "native", "i8_words.cu")
+    nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+    subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_100a,code=sm_100a", "-o", str(exe), src],
+                   check=True, capture_output=True, text=True)
+    assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "ok\n"
