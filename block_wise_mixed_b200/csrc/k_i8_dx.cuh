@@ -307,6 +307,7 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                     mine = __shfl_sync(0xffffffffu, seen, 0) == others;
                 }
                 if (mine) {
+                    __syncwarp();   // what lane 0 acquired holds for all lanes
                     if (lane == 0) *counter = 0u;   // clean for the next call
                     __threadfence();
                 }

@@ -465,6 +465,7 @@ k_i8_stream(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CU
                         mine = __shfl_sync(0xffffffffu, seen, 0) == others;
                     }
                     if (mine) {
+                        __syncwarp();   // what lane 0 acquired holds for all lanes
                         if (lane == 0) *counter = 0u;   // clean for the next call
                         __threadfence();
                     }
