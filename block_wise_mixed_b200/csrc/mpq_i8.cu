@@ -310,6 +310,23 @@ inline size_t dx_slots(int64_t M, int64_t N, int64_t K, int nw) {
     return (size_t)plan_slots(p.work) * 2 * p.nt * 128 * 4;
 }
 
+// The most slots that any call of up to M tokens takes: equal runs (two for each
+// worker) of the widest tiles that M allows.
+inline size_t product_slots_upto(int64_t M, int nw) {
+    int64_t nt = 16;
+    while (nt < 128 && nt < M) nt *= 2;
+    return (size_t)2 * kSMs * nw * nt * 128 * 4;
+}
+inline size_t dx_slots_upto(int64_t M) {
+    int64_t nt = 32;
+    while (nt < 256 && nt < M) nt *= 2;
+    return (size_t)2 * kPairs * 2 * nt * 128 * 4;
+}
+// Rows of gradients (in two parts up to kDxSplitM tokens).
+inline size_t grad_rows_upto(int64_t M) {
+    return (size_t)std::max<int64_t>(M, 2 * std::min<int64_t>(M, kDxSplitM));
+}
+
 inline int64_t grad_ld(int64_t n) { return div_up(n, 64) * 64; }
 
 struct I8Ws {
@@ -346,6 +363,14 @@ I8Ws ws_backward(void* ws, int64_t M, int64_t N, int64_t K, int nw) {
     const size_t row = (size_t)grad_ld(N) * (size_t)nw;
     return carve(ws, std::max(ps, dx_slots(M, N, K, nw)), (size_t)M * grad_parts(M) * row * 2,
                  nw == 2 ? (size_t)M * row * 4 : 0, (size_t)M * 4);
+}
+
+// For any call of up to M tokens: the layouts above with the most that a part may take.
+size_t bytes_product(int64_t M, int nw) { return carve(nullptr, product_slots_upto(M, nw), 0, 0, 0).bytes; }
+size_t bytes_backward(int64_t M, int64_t N, int nw) {
+    const size_t ps = nw == 2 ? product_slots_upto(M, 2) : 0, row = (size_t)grad_ld(N) * (size_t)nw;
+    return carve(nullptr, std::max(ps, dx_slots_upto(M)), grad_rows_upto(M) * row * 2, nw == 2 ? (size_t)M * row * 4 : 0,
+                 (size_t)M * 4).bytes;
 }
 
 // x and the weights of a product: common columns, at least one channel.
@@ -511,16 +536,16 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
 extern "C" {
 
 size_t mpq_i8_linear_workspace_size(int32_t M, int32_t N, int32_t K) {
-    return shape_ok(M, N, K) ? ws_product(nullptr, M, N, K, 1).bytes : 0;
+    return shape_ok(M, N, K) ? bytes_product(M, 1) : 0;
 }
 size_t mpq_i8_gated_workspace_size(int32_t M, int32_t F, int32_t K) {
-    return shape_ok(M, F, K) ? ws_product(nullptr, M, F, K, 2).bytes : 0;
+    return shape_ok(M, F, K) ? bytes_product(M, 2) : 0;
 }
 size_t mpq_i8_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K) {
-    return shape_ok(M, N, K) ? ws_backward(nullptr, M, N, K, 1).bytes : 0;
+    return shape_ok(M, N, K) ? bytes_backward(M, N, 1) : 0;
 }
 size_t mpq_i8_gated_backward_workspace_size(int32_t M, int32_t F, int32_t K) {
-    return shape_ok(M, F, K) ? ws_backward(nullptr, M, F, K, 2).bytes : 0;
+    return shape_ok(M, F, K) ? bytes_backward(M, F, 2) : 0;
 }
 
 mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydtype ydt, int64_t ldy, void* ws,
@@ -532,7 +557,7 @@ mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydty
     if (x->rows == 0) return MPQ_OK;
     const I8Ws k = ws_product(ws, x->rows, w->rows, x->cols, 1);
     st = check_array(y_dev, elem_size(ydt), ldy, w->rows);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, bytes_product(x->rows, 1));
     if (st != MPQ_OK) return st;
     I8Product p{};
     p.y = y_dev;
@@ -550,7 +575,7 @@ mpq_status mpq_i8_gated(const mpq_i8* x, const mpq_i8* w_gate, const mpq_i8* w_u
     if (x->rows == 0) return MPQ_OK;
     const I8Ws k = ws_product(ws, x->rows, w_gate->rows, x->cols, 2);
     st = check_array(h_dev, elem_size(ydt), ldh, w_gate->rows);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, bytes_product(x->rows, 2));
     if (st != MPQ_OK) return st;
     I8Product p{};
     p.y = h_dev;
@@ -569,7 +594,7 @@ mpq_status mpq_i8_linear_backward(const mpq_i8* w, const void* dy_dev, int32_t M
     const I8Ws k = ws_backward(ws, M, w->rows, w->cols, 1);
     st = check_array(dy_dev, 2, lddy, w->rows);
     if (st == MPQ_OK) st = check_array(dx_dev, 2, lddx, w->cols);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, bytes_backward(M, w->rows, 1));
     if (st != MPQ_OK) return st;
     const int64_t ldg = grad_ld(w->rows);
     const bool vec = aligned(dy_dev, 16) && (M == 1 || lddy % 8 == 0);
@@ -596,7 +621,7 @@ mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mp
     if (st == MPQ_OK && d_gate_dev) st = check_array(d_gate_dev, 2, ldd, F);
     if (st == MPQ_OK && d_up_dev) st = check_array(d_up_dev, 2, ldd, F);
     if (st == MPQ_OK) st = check_array(dx_dev, 2, lddx, x->cols);
-    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, k.bytes);
+    if (st == MPQ_OK) st = check_ws(ws, ws_bytes, bytes_backward(x->rows, F, 2));
     if (st != MPQ_OK) return st;
     I8Product p{};
     p.dh = static_cast<const uint16_t*>(dh_dev);

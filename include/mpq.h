@@ -417,8 +417,9 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
  * (the sum is exact in int32, then fp32 in the order written; rounded to
  * nearest-even for MPQ_Y_BF16).  x: M x K, w: N x K; y element (m, n) at
  * m * ldy + n (ldy >= N), aligned to its type.
- *   ws  device workspace of mpq_i8_linear_workspace_size(M, N, K) bytes,
- *       256-byte aligned, zero-filled before its first use: the same rules
+ *   ws  device workspace of mpq_i8_linear_workspace_size(M, N, K) bytes, which
+ *       serves every batch of up to M tokens (a smaller one may be cut into
+ *       more pieces and use more of it), 256-byte aligned, zero-filled before its first use: the same rules
  *       as mpq_linear's (left clean by every call without a device error, so
  *       zero it again only after one).  One workspace of the largest size may
  *       serve all mpq_i8_* calls of a stream, one after another; calls that

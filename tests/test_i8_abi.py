@@ -185,3 +185,13 @@ def test_row_words_end_at_the_last_column(tmp_path):
     subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_100a,code=sm_100a", "-o", str(exe), src],
                    check=True, capture_output=True, text=True)
     assert subprocess.run([str(exe)], capture_output=True, text=True).stdout == "ok\n"
+
+
+@pytest.mark.parametrize("name", ["linear", "gated", "linear_backward", "gated_backward"])
+def test_workspace_of_the_largest_batch_serves_smaller_ones(lib, name):
+    """Sizes never fall as the batch grows, through every change of plan."""
+    f = getattr(lib, "mpq_i8_%s_workspace_size" % name)
+    batches = list(range(0, 140)) + [191, 192, 255, 256, 257, 300, 511, 512, 513, 1000, 2048, 4096, 100000]
+    for N, K in ((1, 1), (96, 64), (1371, 2003), (9728, 16384), (4096, 14336), (19100, 6000), (28672, 8192)):
+        sizes = [f(M, N, K) for M in batches]
+        assert sizes == sorted(sizes), (N, K)
