@@ -7,7 +7,7 @@ package only marshals arguments to it.  The ``i8_*`` calls are the 8-bit integer
 operators for layers that stay at 8 bits throughout: row quantizer, linear, gated
 feed-forward block and their gradients.  ``synth`` draws seeded workloads.
 """
-from ._lib import (ACT_GELU_TANH, ACT_SILU, I8Matrix, i8_dequantize, i8_empty, i8_gated,  # noqa: F401
+from ._lib import (ACT_GELU_TANH, ACT_SILU, I8_WS_ZERO, I8Matrix, i8_dequantize, i8_empty, i8_gated,  # noqa: F401
                    i8_gated_backward, i8_gated_backward_workspace_size, i8_gated_workspace_size, i8_linear,
                    i8_linear_backward, i8_linear_backward_workspace_size, i8_linear_workspace_size, i8_matrix,
                    i8_quantize)

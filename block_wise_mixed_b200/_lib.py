@@ -418,6 +418,7 @@ def table_numpy(P: PackedLayer) -> np.ndarray:
 ACT_SILU, ACT_GELU_TANH = "silu", "gelu_tanh"
 _ACTS = {ACT_SILU: 0, ACT_GELU_TANH: 1}   # mpq_act
 I8_MAX_COLS = 131071                      # MPQ_I8_MAX_COLS
+I8_WS_ZERO = 9984                         # MPQ_I8_WS_ZERO
 
 
 class I8Matrix:
@@ -497,12 +498,15 @@ def _mat(q, where, name, device=None, cols=None):
     return q.device
 
 
-def _new(shape, dtype, device, stream, zero=False):
-    """A tensor for a call on `stream` (None: the current one), allocated on
-    the current stream: the call waits for the memory's earlier uses (and the
-    zero fill), and the memory is not reused before the call is done."""
+def _new(shape, dtype, device, stream, zero=0):
+    """A tensor for a call on `stream` (None: the current one), its first
+    `zero` elements zero, allocated on the current stream: the call waits for
+    the memory's earlier uses (and the zero fill), and the memory is not reused
+    before the call is done."""
     import torch
-    t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if zero:
+        t[:zero].zero_()
     if stream is not None:
         t.record_stream(stream)
         stream.wait_stream(torch.cuda.current_stream(device))
@@ -537,11 +541,13 @@ def _call(name, device, stream, *args):
 
 
 def _call_ws(name, sizes, device, stream, ws, *args):
-    """_call with a workspace: the caller's, or a new zeroed one of the size
-    that `name` asks for at `sizes`."""
+    """_call with a workspace: the caller's, or a new one of the size that
+    `name` asks for at `sizes`.  (A new one is gone after the call, and its
+    error word with it: pass one to use check().)"""
     import torch
     if ws is None:
-        ws = _new((getattr(lib(), name + "_workspace_size")(*sizes),), torch.uint8, device, stream, zero=True)
+        ws = _new((getattr(lib(), name + "_workspace_size")(*sizes),), torch.uint8, device, stream,
+                  I8_WS_ZERO)
     elif not (isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == device):
         _bad(name, "ws must be a contiguous tensor on the device of the others")
     _call(name, device, stream, *args, ws.data_ptr(), ws.nbytes)
@@ -599,7 +605,10 @@ def i8_gated_backward_workspace_size(M: int, F: int, K: int) -> int:
 
 
 def i8_linear(x: I8Matrix, w: I8Matrix, out=None, ws=None, stream=None, ydtype: int = Y_F32):
-    """mpq_i8_linear: y (M x N, fp32 or bf16: out's type, or ydtype) = x_hat * w_hat^T."""
+    """mpq_i8_linear: y (M x N, fp32 or bf16: out's type, or ydtype) = x_hat * w_hat^T.
+    ws (here and below): a workspace whose device errors check() reads, of
+    i8_*_workspace_size bytes, the first I8_WS_ZERO of them zero at first;
+    None takes a new one for the call, whose errors nobody reads."""
     dev = _mat(x, "i8_linear", "x")
     _mat(w, "i8_linear", "w", dev, x.cols)
     out, ld = _out(out, (x.rows, w.rows), dev, "i8_linear", "out", _dtypes(ydtype), stream)

@@ -165,8 +165,10 @@ constexpr int kPairs = kSMs / 2;
 // that a call writes before it reads.  The zeroed part has one size for all
 // mpq_i8_* calls, so one workspace serves them all, one after another.
 constexpr size_t kErrBytes = 256;
-constexpr size_t kI8ZeroBytes = kErrBytes + 9728;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
-static_assert(kSMs * I8S_EPI * 4 <= 9728 && kPairs * 2 * I8X_MAX_EPI * 4 <= 9728 && kI8ZeroBytes % 256 == 0, "counters");
+constexpr size_t kI8ZeroBytes = MPQ_I8_WS_ZERO;   // I8S_EPI counters for each CTA (a pair: 2 I8X_EPI)
+constexpr size_t kCounterBytes = kI8ZeroBytes - kErrBytes;
+static_assert(kSMs * I8S_EPI * 4 <= kCounterBytes && kPairs * 2 * I8X_MAX_EPI * 4 <= kCounterBytes &&
+              kI8ZeroBytes % 256 == 0, "counters");
 
 inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 1 && K >= 1 && K <= MPQ_I8_MAX_COLS;

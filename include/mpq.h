@@ -384,6 +384,9 @@ mpq_status mpq_fold_orders(int32_t n, const int32_t* row_perm_a, const int32_t* 
  * of up to 128 * 128 are exact in 32 bits.  In all calls below outputs must
  * not overlap inputs. */
 #define MPQ_I8_MAX_COLS 131071
+/* The first bytes of an mpq_i8_* workspace, the ones that have to be zero
+ * before its first use; the rest is written before it is read. */
+#define MPQ_I8_WS_ZERO 9984
 typedef struct {
     int32_t rows, cols;
     int64_t ld;
@@ -419,11 +422,13 @@ mpq_status mpq_i8_dequantize(const mpq_i8* q, void* x_dev, mpq_ydtype dt, int64_
  * m * ldy + n (ldy >= N), aligned to its type.
  *   ws  device workspace of mpq_i8_linear_workspace_size(M, N, K) bytes, which
  *       serves every batch of up to M tokens (a smaller one may be cut into
- *       more pieces and use more of it), 256-byte aligned, zero-filled before its first use: the same rules
- *       as mpq_linear's (left clean by every call without a device error, so
- *       zero it again only after one).  One workspace of the largest size may
- *       serve all mpq_i8_* calls of a stream, one after another; calls that
- *       may overlap need their own, and it is not shared with mpq_linear.
+ *       more pieces and use more of it), 256-byte aligned, its first
+ *       MPQ_I8_WS_ZERO bytes zero before its first use: otherwise the same
+ *       rules as mpq_linear's (left clean by every call without a device
+ *       error, so zero them again only after one).  One workspace of the
+ *       largest size may serve all mpq_i8_* calls of a stream, one after
+ *       another; calls that may overlap need their own, and it is not shared
+ *       with mpq_linear.
  * Results do not depend on how the work is split.  Host errors: ARG, SHAPE
  * (columns differ, sizes out of range), WORKSPACE; device (mpq_check):
  * TIMEOUT.  M == 0 is a no-op. */

@@ -195,3 +195,26 @@ def test_workspace_of_the_largest_batch_serves_smaller_ones(lib, name):
     for N, K in ((1, 1), (96, 64), (1371, 2003), (9728, 16384), (4096, 14336), (19100, 6000), (28672, 8192)):
         sizes = [f(M, N, K) for M in batches]
         assert sizes == sorted(sizes), (N, K)
+
+
+def test_header_constants():
+    text = open(B.HEADER).read()
+    for name, value in (("MPQ_I8_MAX_COLS", B.I8_MAX_COLS), ("MPQ_I8_WS_ZERO", B.I8_WS_ZERO)):
+        assert "#define %s %d\n" % (name, value) in text
+
+
+def test_own_workspace_is_zeroed_where_it_has_to_be(lib, monkeypatch):
+    """A call without a workspace clears the first bytes of its own, and no more."""
+    import torch
+    made = []
+    empty = torch.empty
+
+    def poisoned(*a, **k):
+        made.append(empty(*a, **k).fill_(0xAB))
+        return made[-1]
+    monkeypatch.setattr(torch, "empty", poisoned)
+    monkeypatch.setattr(B, "_call", lambda *a: None)
+    B._call_ws("mpq_i8_gated_backward", (300, 1371, 2003), torch.device("cpu"), None, None)
+    ws, = made
+    assert ws.numel() == lib.mpq_i8_gated_backward_workspace_size(300, 1371, 2003)
+    assert bool((ws[:B.I8_WS_ZERO] == 0).all()) and bool((ws[B.I8_WS_ZERO:] == 0xAB).all())
