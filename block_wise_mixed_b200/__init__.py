@@ -10,7 +10,7 @@ feed-forward block and their gradients.  ``synth`` draws seeded workloads.
 from ._lib import (ACT_GELU_TANH, ACT_SILU, I8_WS_ZERO, I8Matrix, i8_dequantize, i8_empty, i8_gated,  # noqa: F401
                    i8_gated_backward, i8_gated_backward_workspace_size, i8_gated_workspace_size, i8_linear,
                    i8_linear_backward, i8_linear_backward_workspace_size, i8_linear_workspace_size, i8_matrix,
-                   i8_quantize)
+                   i8_plan, i8_quantize)
 from ._lib import (GROUP_MAX, Y_BF16, Y_F32, MpqError, PackedLayer, allocate_bits, check, fold_orders,  # noqa: F401
                    linear,
                    linear_group, linear_group_workspace_size, linear_host, linear_host_workspace_size,

@@ -55,6 +55,11 @@ class I8(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class I8Work(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kernel", "columns", "workers", "full", "rem", "cuts", "cluster")] + \
+               [("slots", ctypes.c_uint64)]
+
+
 _lib = None
 
 
@@ -138,6 +143,8 @@ def load(path: str):
         getattr(D, f).restype = cint
         getattr(D, f + "_workspace_size").argtypes = [i32, i32, i32]
         getattr(D, f + "_workspace_size").restype = sz
+    D.mpq_i8_plan.argtypes = [cint, i32, i32, i32, ctypes.POINTER(I8Work)]
+    D.mpq_i8_plan.restype = cint
     D.mpq_i8_quantize.restype = cint
     D.mpq_i8_dequantize.restype = cint
     D.mpq_check.argtypes = [P, P]
@@ -602,6 +609,24 @@ def i8_linear_backward_workspace_size(M: int, N: int, K: int) -> int:
 
 def i8_gated_backward_workspace_size(M: int, F: int, K: int) -> int:
     return lib().mpq_i8_gated_backward_workspace_size(M, F, K)
+
+
+_OPS = ("linear", "gated", "linear_backward", "gated_backward")   # mpq_i8_op
+_KERNELS = {1: "stream", 2: "tile", 3: "dx"}                       # mpq_i8_kernel
+
+
+def i8_plan(op: str, M: int, N: int, K: int) -> dict:
+    """mpq_i8_plan: how the call `op` ("linear", "gated", "linear_backward",
+    "gated_backward") lays out its work for M tokens, N (F) channels and K
+    columns: {"product": {...}, "gradient": {...}} of the parts that it has."""
+    if op not in _OPS:
+        _bad("i8_plan", "op must be one of %s" % (_OPS,))
+    out = (I8Work * 2)()
+    st = lib().mpq_i8_plan(_OPS.index(op), M, N, K, out)
+    if st:
+        raise MpqError(st, "mpq_i8_plan")
+    return {part: dict({n: getattr(w, n) for n, _ in I8Work._fields_}, kernel=_KERNELS[w.kernel])
+            for part, w in zip(("product", "gradient"), out) if w.kernel}
 
 
 def i8_linear(x: I8Matrix, w: I8Matrix, out=None, ws=None, stream=None, ydtype: int = Y_F32):

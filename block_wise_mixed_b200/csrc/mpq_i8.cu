@@ -550,6 +550,31 @@ size_t mpq_i8_gated_backward_workspace_size(int32_t M, int32_t F, int32_t K) {
     return shape_ok(M, F, K) ? bytes_backward(M, F, 2) : 0;
 }
 
+mpq_status mpq_i8_plan(mpq_i8_op op, int32_t M, int32_t N, int32_t K, mpq_i8_work* out) {
+    if (!out || op < MPQ_I8_LINEAR || op > MPQ_I8_GATED_BACKWARD) return MPQ_ERR_ARG;
+    if (M < 1 || !shape_ok(M, N, K)) return MPQ_ERR_SHAPE;
+    out[0] = out[1] = mpq_i8_work{};
+    const int nw = op == MPQ_I8_GATED || op == MPQ_I8_GATED_BACKWARD ? 2 : 1;
+    auto fill = [](mpq_i8_work& o, int kernel, int columns, const I8Plan& p, size_t slots) {
+        o = {kernel, columns, p.workers, p.full, p.rem, p.cuts, p.cluster, slots};
+    };
+    if (op != MPQ_I8_LINEAR_BACKWARD) {
+        const ProductPlan p = product_plan(M, N, K, nw);
+        if (p.nt) {
+            fill(out[0], MPQ_I8_KERNEL_STREAM, p.nt, p.work, product_slots(M, N, K, nw));
+        } else {
+            const int64_t tiles = div_up(M, 256) * div_up(N, 256 / nw);
+            const int workers = (int)std::min<int64_t>(kPairs, tiles);
+            fill(out[0], MPQ_I8_KERNEL_TILE, 256, {(int)(tiles / workers), (int)(tiles % workers), 1, workers, 0}, 0);
+        }
+    }
+    if (op >= MPQ_I8_LINEAR_BACKWARD) {
+        const DxPlan p = dx_plan(M, N, K, nw);
+        fill(out[1], MPQ_I8_KERNEL_DX, p.nt, p.work, dx_slots(M, N, K, nw));
+    }
+    return MPQ_OK;
+}
+
 mpq_status mpq_i8_linear(const mpq_i8* x, const mpq_i8* w, void* y_dev, mpq_ydtype ydt, int64_t ldy, void* ws,
                          size_t ws_bytes, void* stream) {
     const mpq_i8* wl[1] = {w};

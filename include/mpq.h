@@ -473,6 +473,29 @@ mpq_status mpq_i8_gated_backward(const mpq_i8* x, const mpq_i8* w_gate, const mp
                                  int64_t ldd, void* dx_dev, int64_t lddx, void* ws, size_t ws_bytes,
                                  void* stream);
 
+/* Host only.  How a call's work is laid out: out[0] the product of mpq_i8_linear
+ * or of the gated calls, out[1] the gradient product of the backward calls (a
+ * part that the call does not have is all zeros).  For M tokens, N channels (F)
+ * and K columns.  Errors: ARG (op, out), SHAPE (sizes out of range, M < 1). */
+typedef enum {
+    MPQ_I8_LINEAR = 0,
+    MPQ_I8_GATED = 1,
+    MPQ_I8_LINEAR_BACKWARD = 2,
+    MPQ_I8_GATED_BACKWARD = 3
+} mpq_i8_op;
+typedef enum { MPQ_I8_KERNEL_STREAM = 1, MPQ_I8_KERNEL_TILE = 2, MPQ_I8_KERNEL_DX = 3 } mpq_i8_kernel;
+typedef struct {
+    int32_t kernel;    /* mpq_i8_kernel */
+    int32_t columns;   /* of a tile: tokens, or their parts */
+    int32_t workers;   /* CTAs (STREAM) or pairs of CTAs */
+    int32_t full;      /* rounds of whole tiles that every worker takes */
+    int32_t rem;       /* tiles left after them */
+    int32_t cuts;      /* pieces of each of those; 0: equal runs over all of them */
+    int32_t cluster;   /* the pieces are a cluster that adds through shared memory */
+    uint64_t slots;    /* bytes of partial sums in the workspace */
+} mpq_i8_work;
+mpq_status mpq_i8_plan(mpq_i8_op op, int32_t M, int32_t N, int32_t K, mpq_i8_work* out);
+
 /* Synchronizes `stream` and returns the device error word of `ws`: the first
  * device error of the mpq_linear calls on that workspace since it was
  * zero-filled or since the previous mpq_check, or of the last mpq_pack
