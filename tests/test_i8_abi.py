@@ -218,3 +218,47 @@ def test_own_workspace_is_zeroed_where_it_has_to_be(lib, monkeypatch):
     ws, = made
     assert ws.numel() == lib.mpq_i8_gated_backward_workspace_size(300, 1371, 2003)
     assert bool((ws[:B.I8_WS_ZERO] == 0).all()) and bool((ws[B.I8_WS_ZERO:] == 0xAB).all())
+
+
+def test_plan_arguments(lib):
+    work = (B.I8Work * 2)()
+    assert ctypes.sizeof(B.I8Work) == 40
+    assert status(lib.mpq_i8_plan(0, 1, 1, 1, None)) == "MPQ_ERR_ARG"
+    for op in (-1, 4):
+        assert status(lib.mpq_i8_plan(op, 1, 1, 1, work)) == "MPQ_ERR_ARG"
+    for bad in ((0, 1, 1), (-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 131072)):
+        assert status(lib.mpq_i8_plan(0, *bad, work)) == "MPQ_ERR_SHAPE"
+    with pytest.raises(B.MpqError):
+        B.i8_plan("dequantize", 1, 1, 1)
+    for op, parts in (("linear", ["product"]), ("gated", ["product"]), ("linear_backward", ["gradient"]),
+                      ("gated_backward", ["product", "gradient"])):
+        for shape in ((1, 1, 1), (2 ** 31 - 1, 1, 1), (1, 2 ** 31 - 1, 16), (700, 5000, 3000)):
+            assert list(B.i8_plan(op, *shape)) == parts
+
+
+def test_shapes_of_every_plan(lib):
+    """Each shape of i8_shapes.py is handed out the way it is listed for, and no
+    shape in a wide sweep takes a way that has none listed."""
+    import random
+
+    import i8_shapes
+    listed = set()
+    for op, part, kernel, columns, how, M, N, K in i8_shapes.cases():
+        assert i8_shapes.classes(B.i8_plan(op, M, N, K))[part] == (kernel, columns, how), (op, M, N, K)
+        listed.add((op, part, kernel, columns, how))
+    rng = random.Random(11)
+    for _ in range(60000):
+        op = rng.choice(("linear", "gated", "linear_backward", "gated_backward"))
+        M, N, K = (int(round(2 ** rng.uniform(a, b))) for a, b in ((0, 12), (0, 15), (0, 15)))
+        for part, way in i8_shapes.classes(B.i8_plan(op, M, N, K)).items():
+            assert (op, part, *way) in listed, (op, M, N, K)
+
+
+@pytest.mark.parametrize("name", ["linear", "gated", "linear_backward", "gated_backward"])
+def test_workspace_holds_what_the_plan_takes(lib, name):
+    """Partial sums of every batch fit behind the zeroed part of the size for larger ones."""
+    f = getattr(lib, "mpq_i8_%s_workspace_size" % name)
+    for N, K in ((96, 64), (1371, 2003), (9728, 16384), (4096, 14336), (19100, 6000), (28672, 8192), (128000, 4096)):
+        for M in list(range(1, 140)) + [200, 255, 256, 257, 300, 511, 512, 1000, 2048, 4096]:
+            need = max(w["slots"] for w in B.i8_plan(name, M, N, K).values())
+            assert B.I8_WS_ZERO + need <= f(M, N, K), (M, N, K)
