@@ -32,9 +32,11 @@
 // codes and 16 KB of tokens in, reads the codes, writes and reads 16 KB of
 // operand and reads 16 KB of tokens, 80 KB or 640 cycles where the tensor cores
 // need 512; 32 tokens take 104 KB for 16 KB of codes, 830 cycles where HBM needs
-// 700.  Measured: 2048 tokens, 4096 x 14336 175 us, 1.38 PFLOP/s (tensor pipes
-// 73% active, clocks down to 1.6 GHz by power); 16 tokens, 8192 x 28672 56 us,
-// 4.2 TB/s.
+// 700.  Measured with k_i8_grad_rows, on a cool GPU and in a sustained loop: 2048
+// tokens, 4096 x 14336 179 and 215 us, 1.34 and 1.12 PFLOP/s (tensor pipes 74%
+// active, clocks down to 1.6 GHz by power; 448 tiles on 74 pairs are six rounds
+// and four tiles, so a seventh of the time is a round for these four); 16
+// tokens, 8192 x 28672 56 and 61 us, 4.2 and 3.8 TB/s.
 //
 // Work is handed to the pairs as in k_i8_stream; the fp32 partial sums of a
 // cut tile are added in the order of the pieces by the last contributor,
@@ -456,8 +458,8 @@ struct I8GradParams {
 // units between the two passes; what is beyond them is read again.
 // SRC 0: rows of dy start at 16-byte blocks.
 // Bound by its bytes where they are many (512 tokens, gate and up of 14336: 59 MB
-// in, 29 out, mostly through L2, and the product's fp32 stores: 16 us of 189) and
-// by latency where they are few (1 to 2 us).
+// in, 29 out: 22 us from HBM; with the product's fp32 stores 16 us of 189 in its
+// place between the products) and by latency where they are few (1 to 3 us).
 template <int SRC>
 __global__ void __launch_bounds__(1024) k_i8_grad_rows(I8GradParams p) {
     constexpr int KEEP = 4;
