@@ -72,6 +72,7 @@ struct I8DxCfg {
     // take stages in turn: 19 warps leave a thread 96 registers.
     static constexpr int EPI = NT == 32 ? 4 : 8;
     static constexpr int GROUPS = NT == 32 ? 3 : 2;
+    static constexpr int PIECES = NT == 32 ? 1 : NT / (8 * EPI);   // 32-column pieces of a finishing warp
     static constexpr int WARPS = 3 + EPI + GROUPS * I8X_GWARPS;
 };
 
@@ -81,6 +82,7 @@ struct I8DxSmem {
     uint8_t a[Cfg::S][Cfg::U * I8X_A];      // 1024-aligned
     uint8_t b[Cfg::S][Cfg::U * Cfg::B_STRIDE];
     uint8_t raw[Cfg::R][Cfg::U * I8X_RAW];
+    float unscale[Cfg::EPI][Cfg::PIECES * 32];   // of each finishing warp's columns
     uint64_t raw_full[Cfg::R], raw_empty[Cfg::R];
     uint64_t full[Cfg::S], empty[Cfg::S];   // full: both operands of the pair, in the first CTA
     uint64_t d_full[2], d_empty[2], drain;
@@ -258,9 +260,18 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
     } else if (warp < 2 + EPI) {
         const int quad = warp & 3, half = (warp - 2) >> 2;   // columns 32 half .., every 8 EPI
         const uint32_t empty_bar = cluster_addr(&sm.d_empty[0], 0);
+        float* unscale = sm.unscale[warp - 2];
         for (int seg = 0; seg < n_segs; ++seg) {
             const I8Seg g = work.seg(seg);
             const int buf = seg & 1;
+            const int64_t k = (g.tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (g.tile % TM) * tok;
+            const int mc = (int)min((int64_t)tok, p.M - m0);
+#pragma unroll
+            for (int i = 0; i < Cfg::PIECES; ++i) {   // while the tile is multiplied
+                const int c = 32 * half + 8 * EPI * i + lane;
+                unscale[32 * i + lane] = c < mc ? p.unscale[m0 + c] : 0.f;
+            }
+            __syncwarp();
             bool ok = !sm.abort_flag && i8_wait(&sm.d_full[buf], (uint32_t)(seg >> 1) & 1u);
             ok = __all_sync(0xffffffffu, ok && !sm.abort_flag);
             if (!ok) {
@@ -268,8 +279,6 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
                 break;
             }
             i8_fence_after();
-            const int64_t k = (g.tile / TM) * 256 + rank * 128 + quad * 32 + lane, m0 = (g.tile % TM) * tok;
-            const int mc = (int)min((int64_t)tok, p.M - m0);
             const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * NT);
             const int c0 = g.c0, c1 = g.c1;
             auto slot_of = [&](int c) {
@@ -332,9 +341,15 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] += t[i];
                     }
-                    const float us = c + lane < mc ? p.unscale[m0 + c + lane] : 0.f;
+                    const float4* us = reinterpret_cast<const float4*>(unscale + (c - 32 * half) / EPI * 4);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, us, i);
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 s = us[i];
+                        v[4 * i] *= s.x;
+                        v[4 * i + 1] *= s.y;
+                        v[4 * i + 2] *= s.z;
+                        v[4 * i + 3] *= s.w;
+                    }
                     if (k < p.K) {
                         uint16_t* dx = p.dx + (m0 + c) * p.lddx + k;
                         const int left = mc - c;
@@ -439,6 +454,8 @@ k_i8_dx(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUten
 // ---------------------------------------------------------------------------
 // The gradients as the product's operand: rows of fp16 in one part or two.
 // ---------------------------------------------------------------------------
+constexpr int I8G_WARPS = 8;    // of a block with a warp a token
+
 struct I8GradParams {
     const void* src;       // SRC 0, 1: dy in bf16, M x N; 2: scaled fp32 gradients, laid out as g
     int64_t ld;
@@ -447,29 +464,32 @@ struct I8GradParams {
     int64_t ldg, up_off;
     int64_t lo_off;        // the second parts, at + lo_off (0: none)
     float* unscale;        // [M]: what brings a token's sums back
-    int N, cluster;        // channels; blocks of a token
+    int M, N, cluster;     // tokens, channels; blocks of a token
 };
 
-// A block a token, or a cluster of blocks for few tokens: its values times the channels' scales (SRC 2: already done),
-// the largest finite magnitude, and the fp16 parts of the values times the power
-// of two that takes that magnitude into [2^14, 2^15) (2^126 at most, which
-// leaves smaller values exact or with their 11 bits all the same).
-// A thread takes 8 neighbouring columns at a time and keeps its first four such
-// units between the two passes; what is beyond them is read again.
+// A warp, a block or a cluster of blocks a token: its values times the channels'
+// scales (SRC 2: already done), the largest finite magnitude, and the
+// fp16 parts of the values times the power of two that takes that magnitude into
+// [2^14, 2^15) (2^126 at most, which leaves smaller values exact or with their 11
+// bits all the same).  A thread takes 8 neighbouring columns at a time and keeps
+// its first four such units between the two passes; what is beyond them is read
+// again.
 // SRC 0: rows of dy start at 16-byte blocks.
 // Bound by its bytes where they are many (512 tokens, gate and up of 14336: 59 MB
 // in, 29 out: 22 us from HBM; with the product's fp32 stores 16 us of 189 in its
 // place between the products) and by latency where they are few (1 to 3 us).
-template <int SRC>
-__global__ void __launch_bounds__(1024) k_i8_grad_rows(I8GradParams p) {
+template <int SRC, bool WARP>
+__global__ void __launch_bounds__(WARP ? I8G_WARPS * 32 : 1024) k_i8_grad_rows(I8GradParams p) {
     constexpr int KEEP = 4;
     __shared__ uint32_t red[32], top_of;
-    const int64_t m = blockIdx.x / p.cluster;
-    const int first = (int)(blockIdx.x % p.cluster * blockDim.x + threadIdx.x), step = (int)blockDim.x * p.cluster;
+    const int64_t m = WARP ? (int64_t)blockIdx.x * I8G_WARPS + (threadIdx.x >> 5) : blockIdx.x / p.cluster;
+    const int first = WARP ? threadIdx.x & 31 : (int)(blockIdx.x % p.cluster * blockDim.x + threadIdx.x);
+    const int step = WARP ? 32 : (int)blockDim.x * p.cluster;
     const int per = (p.N - 1) / 8 + 1, units = SRC == 2 ? 2 * per : per;
     const bool s_vec = (reinterpret_cast<uintptr_t>(p.s) & 15) == 0;
     pdl_wait();
     pdl_launch_dependents();
+    if (WARP && m >= p.M) return;
 
     auto offset = [&](int u) { return SRC == 2 && u >= per ? p.up_off + (int64_t)(u - per) * 8 : (int64_t)u * 8; };
     auto load = [&](int u, float (&f)[8]) {
@@ -519,16 +539,18 @@ __global__ void __launch_bounds__(1024) k_i8_grad_rows(I8GradParams p) {
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
         if (first + i * step < units) fold(kept[i]);
-    for (int64_t u = (int64_t)first + KEEP * step; u < units; u += step) {
+    for (int64_t u = (int64_t)first + KEEP * step; !WARP && u < units; u += step) {
         float f[8];
         load((int)u, f);
         fold(f);
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < blockDim.x / 32 ? red[threadIdx.x & 31] : 0u);
-    if (p.cluster > 1) {
+    if (!WARP) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+        __syncthreads();
+        top = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < blockDim.x / 32 ? red[threadIdx.x & 31] : 0u);
+    }
+    if (!WARP && p.cluster > 1) {
         if (threadIdx.x == 0) top_of = top;
         cluster_sync();
         const uint32_t a = smem_u32(&top_of);
@@ -558,7 +580,7 @@ __global__ void __launch_bounds__(1024) k_i8_grad_rows(I8GradParams p) {
 #pragma unroll
     for (int i = 0; i < KEEP; ++i)
         if (first + i * step < units) put(first + i * step, kept[i]);
-    for (int64_t u = (int64_t)first + KEEP * step; u < units; u += step) {
+    for (int64_t u = (int64_t)first + KEEP * step; !WARP && u < units; u += step) {
         float f[8];
         load((int)u, f);
         put((int)u, f);

@@ -490,24 +490,37 @@ mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg
                                    stream, w0, w1, g0, g1, p, plan);
 }
 
-// The operand of the gradient product from `src` (SRC as in k_i8_grad_rows).  A thread
-// takes one unit of 8 columns while the SMs have threads enough for all, four at
-// most (256 tokens of 4096 channels, whole gradient: 22.9 us, 25.6 with four);
-// more than 1024 threads a token are a cluster (128000 channels).
+// The operand of the gradient product from `src` (SRC as in k_i8_grad_rows).  Many
+// short tokens take a warp each (3840 of 64 channels, whole gradient: 9.4 us, 12.2
+// with blocks; 64 of 1024: 18.6, 15.5 with blocks).  For others a thread takes
+// one unit of 8 columns if all blocks are resident so, else two to four (256
+// tokens of 4096 channels: 22.8 us, 25.6 with four; 125 of 18560: 50.5 us with
+// two blocks a token in two waves, 47.1 with one); more than 1024 threads a token
+// are a cluster, and so are more than 256 where the gradients are more than L2
+// holds and smaller blocks keep HBM busier (2240 tokens, gate and up of 22528:
+// 583 us, 619 with 1024 threads).
 template <int SRC>
 mpq_status grad_rows_run(I8GradParams& p, const I8Ws& ws, int64_t M, int64_t N, int64_t ldg, void* stream) {
     p.g = ws.grads;
     p.ldg = ldg;
     p.lo_off = grad_parts(M) == 2 ? M * ldg : 0;
     p.unscale = ws.unscale;
+    p.M = (int)M;
     p.N = (int)N;
     const int64_t units = div_up(N, 8) * (SRC == 2 ? 2 : 1);
-    const int64_t warps = div_up(units, 32 * std::clamp<int64_t>(div_up(M * units, kSMs * 1024), 1, 4));
-    p.cluster = 1;
-    while (p.cluster < 8 && p.cluster * 32 < warps) p.cluster *= 2;
-    const int threads = (int)std::min<int64_t>(1024, div_up(warps, p.cluster) * 32);
-    return launch_cluster(p.cluster > 1 ? p.cluster : 0, k_i8_grad_rows<SRC>, dim3((unsigned)(M * p.cluster)), threads, 0,
-                          stream, p);
+    if (units <= 4 * 32 && M >= 8 * kSMs)
+        return launch(k_i8_grad_rows<SRC, true>, dim3((unsigned)div_up(M, I8G_WARPS)), I8G_WARPS * 32, 0, stream, p);
+    const int most = M * units * 8 * (SRC == 2 ? 4 : 2) > (int64_t)126 << 20 ? 8 : 32;   // warps of a block
+    int threads = 0;
+    for (int each = 1; each <= 4; ++each) {
+        const int64_t warps = div_up(units, 32 * each);
+        p.cluster = 1;
+        while (p.cluster < 8 && p.cluster * most < warps) p.cluster *= 2;
+        threads = (int)std::min<int64_t>(1024, div_up(warps, p.cluster) * 32);
+        if (M * p.cluster <= (int64_t)kSMs * (1024 / threads)) break;
+    }
+    return launch_cluster(p.cluster > 1 ? p.cluster : 0, k_i8_grad_rows<SRC, false>, dim3((unsigned)(M * p.cluster)), threads,
+                          0, stream, p);
 }
 
 mpq_status dx_run(const mpq_i8* const* w, int nw, const uint16_t* g, int64_t ldg, int64_t up_off, int64_t M,
