@@ -20,8 +20,8 @@
 //
 // Measured on a cool GPU and in a sustained loop (clocks down by power): 2048
 // tokens, gate and up 14336 x 4096 152 and 177 us, 3.2 and 2.7 P op/s (tensor pipes
-// active 82% of the time when cool); 4096 x 14336 79 and 95 us, 3.0 and 2.5 P op/s
-// (69%: 128 tiles on 74 pairs take two rounds for 1.73).
+// active 80% of the time when cool); 4096 x 14336 79 and 95 us, 3.0 and 2.5 P op/s
+// (68%: 128 tiles on 74 pairs take two rounds for 1.73).
 #pragma once
 #include "k_i8_stream.cuh"
 
